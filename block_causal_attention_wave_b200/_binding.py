@@ -40,7 +40,17 @@ class Rope(ctypes.Structure):
                 ("base", ctypes.c_float)]
 
 
-ACT_NONE, ACT_GELU_TANH = 0, 1
+class RotarySpec(ctypes.Structure):
+    _fields_ = [("pairs", ctypes.c_int32 * 3), ("base", ctypes.c_float),
+                ("layout", ctypes.c_int32), ("ladder", ctypes.c_int32),
+                ("inverse", ctypes.c_int32)]
+
+
+ACT_NONE, ACT_GELU_TANH, ACT_GELU_ERF, ACT_SILU = 0, 1, 2, 3
+ACTIVATIONS = {"none": ACT_NONE, "gelu_tanh": ACT_GELU_TANH, "gelu_erf": ACT_GELU_ERF,
+               "silu": ACT_SILU}
+ROTARY_LAYOUTS = {"interleaved": 0, "halves": 1}
+ROTARY_LADDERS = {"axis": 0, "ladder": 1}
 KV_BF16, KV_FP8_E4M3 = 0, 1
 
 
@@ -106,6 +116,30 @@ _SIGS = {
     "wave_linear": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                    ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
                                    ctypes.c_void_p, ctypes.c_void_p]),
+    "wave_linear_bias": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                        ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                        ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_void_p]),
+    "wave_rotary": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(RotarySpec), ctypes.c_void_p,
+                                   ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                   ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                   ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
+                                   ctypes.c_int64, ctypes.c_void_p]),
+    "wave_kv_write_tokens": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(Node),
+                                            ctypes.POINTER(ctypes.c_int32),
+                                            ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                            ctypes.c_void_p]),
+    "wave_token_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(Node), ctypes.c_int32,
+                                       ctypes.c_int32, ctypes.POINTER(ctypes.c_int32),
+                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
+    "wave_token_attn_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(Node),
+                                                 ctypes.c_int32, ctypes.c_int32,
+                                                 ctypes.POINTER(ctypes.c_int32), ctypes.c_int32,
+                                                 ctypes.POINTER(ctypes.c_uint64)]),
     "wave_kv_append_batch": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(Node),
                                             ctypes.POINTER(ctypes.c_void_p),
                                             ctypes.POINTER(ctypes.c_void_p),
@@ -175,6 +209,12 @@ def _nodes(active):
     for i, (c, l) in enumerate(active):
         arr[i].chunk, arr[i].level = int(c), int(l)
     return arr
+
+
+def _ints(values, n, what):
+    if len(values) != n:
+        raise ValueError(f"{what}: {n} values wanted, got {len(values)}")
+    return (ctypes.c_int32 * max(1, n))(*values)
 
 
 def _stream_handle(stream):
@@ -348,6 +388,133 @@ class KVCache:
                                     int(act), ctypes.c_void_p(Y.data_ptr()),
                                     _stream_handle(stream)))
         return Y
+
+    def _rows(self, t, what, rows, width, dtype="torch.bfloat16"):
+        """(address, row stride) of a CUDA tensor read as ``rows`` rows of
+        ``width`` contiguous elements: 2-D [rows][width], or [rows][heads][d]
+        with contiguous heads. A kernel would read a host tensor's address, or
+        past a short one, as readily as a good one, so both are refused here."""
+        if str(t.dtype) != dtype or t.device != self.pool.device:
+            raise ValueError(f"{what}: a {dtype} tensor on {self.pool.device} is wanted, got "
+                             f"{t.dtype} on {t.device}")
+        shape, stride = t.shape, t.stride()
+        ok = shape[0] == rows and len(shape) in (2, 3) and stride[-1] == 1
+        if len(shape) == 3:
+            ok = ok and shape[1] * shape[2] == width and (shape[1] == 1 or stride[1] == shape[2])
+        else:
+            ok = ok and shape[-1] == width
+        if not ok:
+            raise ValueError(f"{what}: {rows} rows of {width} contiguous elements are wanted, got "
+                             f"shape {tuple(shape)}, strides {tuple(stride)}")
+        return t.data_ptr(), stride[0] if rows > 1 else width
+
+    def _device(self):
+        if self.pool is None:
+            raise WaveError(ERR_ARG, "host-only handle (pool == NULL)")
+
+    def linear_bias(self, A, W, Y, bias=None, R=None, act="none", stream=None):
+        """Y [M][N] = act(A W^T + bias) (+ R) for A [M][K], W [N][K], bias [N], R
+        [M][N]; A, R and Y may have row strides (multiples of 8), Y may be R.
+        ``act``: "none", "gelu_tanh", "gelu_erf" or "silu" (or an ACT_* code)."""
+        self._device()
+        M, K = A.shape
+        N = W.shape[0]
+        a, lda = self._rows(A, "A", M, K)
+        w, ldw = self._rows(W, "W", N, K)
+        y, ldy = self._rows(Y, "Y", M, N)
+        if N > 1 and ldw != K:
+            raise ValueError("W must be contiguous")
+        b = self._rows(bias.view(1, -1), "bias", 1, N)[0] if bias is not None else None
+        r, ldr = self._rows(R, "R", M, N) if R is not None else (None, 0)
+        code = ACTIVATIONS[act] if isinstance(act, str) else int(act)
+        _check(self.lib.wave_linear_bias(self.h, a, lda, M, K, w, N, b, r, ldr, code, y, ldy,
+                                         _stream_handle(stream)))
+        return Y
+
+    def rotary(self, positions, Q, K=None, Qout=None, Kout=None, pairs=None, base=10000.0,
+               layout="interleaved", ladder="axis", inverse=False, stream=None):
+        """Turn Q [rows][q_heads][d] (and K) by ``positions`` (int32 [rows][3]
+        on the device) into Qout (and Kout); without outputs, in place. ``pairs``:
+        rotation pairs per axis (default: wave_rope's split of d/2);
+        ``layout``: "interleaved" or "halves"; ``ladder``: "axis" (each axis
+        its own frequencies) or "ladder" (one over the head); ``inverse``:
+        turn back, which is the gradient of turning."""
+        self._device()
+        rows, d = Q.shape[0], self.head_dim
+        if pairs is None:
+            pairs = (d // 2 - 2 * (d // 6), d // 6, d // 6)
+        if Q.shape[-1] != d or (K is not None and K.shape[-1] != d):
+            raise ValueError(f"Q and K are [rows][heads][{d}]")
+        if Qout is None:
+            Qout = Q
+        if K is not None and Kout is None:
+            Kout = K
+        p, ldp = self._rows(positions, "positions", rows, 3, "torch.int32")
+        if rows > 1 and ldp != 3:
+            raise ValueError("positions must be contiguous")
+        qh = Q.shape[1]
+        q, ldq = self._rows(Q, "Q", rows, qh * d)
+        qo, ldqo = self._rows(Qout, "Qout", rows, qh * d)
+        k = ko = None
+        ldk = ldko = kh = 0
+        if K is not None:
+            kh = K.shape[1]
+            k, ldk = self._rows(K, "K", rows, kh * d)
+            ko, ldko = self._rows(Kout, "Kout", rows, kh * d)
+        spec = RotarySpec((ctypes.c_int32 * 3)(*pairs), base, ROTARY_LAYOUTS[layout],
+                          ROTARY_LADDERS[ladder], int(bool(inverse)))
+        _check(self.lib.wave_rotary(self.h, ctypes.byref(spec), p, rows, q, ldq, qh, qo, ldqo, k,
+                                    ldk, kh, ko, ldko, _stream_handle(stream)))
+        return (Qout, Kout) if K is not None else Qout
+
+    def write_tokens(self, entries, first, K, V, counts=None, stream=None):
+        """Write tokens first[i] .. first[i] + counts[i] - 1 of entry i; K and V
+        [sum of counts][H][d] hold the entries' tokens one after another
+        (``counts``: one each by default). Entries need pages (alloc)."""
+        self._device()
+        n = len(entries)
+        counts = [1] * n if counts is None else counts
+        width, rows = self.heads * self.head_dim, sum(counts)
+        k, ldk = self._rows(K, "K", rows, width)
+        v, ldv = self._rows(V, "V", rows, width)
+        _check(self.lib.wave_kv_write_tokens(self.h, n, _nodes(entries), _ints(first, n, "first"),
+                                             _ints(counts, n, "counts"), k, ldk, v, ldv,
+                                             _stream_handle(stream)))
+
+    def token_attn_workspace(self, active, policy, own_tokens=None, q_heads=None) -> int:
+        """Workspace bytes that token_attn needs for these arguments (may be 0)."""
+        n = len(active)
+        own = _ints(own_tokens, n, "own_tokens") if own_tokens is not None else None
+        b = ctypes.c_uint64(0)
+        _check(self.lib.wave_token_attn_workspace(self.h, _nodes(active), n, _policy(policy), own,
+                                                  q_heads or self.heads, ctypes.byref(b)))
+        return b.value
+
+    def token_attn(self, active, policy, Q, O, own_tokens=None, lse=None, workspace=None,
+                   stream=None):
+        """O [n][q_heads][d] = attention of one query token per listed node over
+        its key list, the own entry up to own_tokens[i] tokens (None: whole
+        entries); ``lse`` (float32 [n][q_heads]) receives the log-sum-exp;
+        ``workspace`` is a CUDA tensor of token_attn_workspace() bytes."""
+        self._device()
+        n = len(active)
+        q_heads = Q.shape[1]
+        own = _ints(own_tokens, n, "own_tokens") if own_tokens is not None else None
+        q, ldq = self._rows(Q, "Q", n, q_heads * self.head_dim)
+        o, ldo = self._rows(O, "O", n, q_heads * self.head_dim)
+        s = None
+        if lse is not None:
+            s, lds = self._rows(lse, "lse", n, q_heads, "torch.float32")
+            if n > 1 and lds != q_heads:
+                raise ValueError("lse must be contiguous")
+        ws, nbytes = None, 0
+        if workspace is not None:
+            if workspace.device != self.pool.device or not workspace.is_contiguous():
+                raise ValueError(f"workspace: a contiguous tensor on {self.pool.device} is wanted")
+            ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _check(self.lib.wave_token_attn(self.h, _nodes(active), n, _policy(policy), own, q_heads, q,
+                                        ldq, o, ldo, s, ws, nbytes, _stream_handle(stream)))
+        return O
 
     def release(self, chunk, level):
         _check(self.lib.wave_kv_release(self.h, chunk, level))

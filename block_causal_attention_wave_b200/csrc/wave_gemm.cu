@@ -88,6 +88,8 @@ struct GemmParams {
   int32_t act;             // 0 none, 1 tanh-GELU
   uint16_t* y;
   const uint16_t* resid;   // R [M][N] or null
+  const uint16_t* bias;    // the form with bias: [N] or null
+  int64_t ldr, ldy;        // the form with bias: row strides of R and Y
   // MODE_QKV: node i's rows are A rows i T .. i T + T - 1; its m-tile j
   // (ceil(T / 128) per node) is page pages[i * mt_per_node + j].
   uint16_t* q;             // Q [n T][H][128]
@@ -132,6 +134,15 @@ __device__ __forceinline__ int64_t a_row0(const GemmParams& p, int mt) {
   return (int64_t)mt * 128;
 }
 
+// GELU, erf form, and SiLU (the form with bias).
+__device__ __forceinline__ float gelu_erf(float x) {
+  return 0.5f * x * (1.f + erff(0.7071067811865476f * x));
+}
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+
+// BIAS: MODE_LINEAR with a bias, row strides, every activation and an N that
+// need not fill a tile (N a multiple of 8).
+template <bool BIAS>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_wide_kernel(const __grid_constant__ GemmParams p) {
   using C = GemmCfg;
@@ -238,7 +249,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const int mt = t / n_n, nt = t - mt * n_n;
-      if (p.mode == MODE_LINEAR) {
+      if constexpr (BIAS) {
+        const int64_t r = (int64_t)mt * 128 + row;
+        const bool in = r < p.M;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          const int col0 = nt * 256 + 32 * c;
+          if (col0 >= p.N) break;
+          uint32_t v[32];
+          tmem_ld32_wait(trow + 256 * acc + 32 * c, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (col0 + 8 * j < p.N && in) {
+              float f[8];
+              uint4 b4 = make_uint4(0, 0, 0, 0), r4 = make_uint4(0, 0, 0, 0);
+              if (p.bias) b4 = *reinterpret_cast<const uint4*>(p.bias + col0 + 8 * j);
+              if (p.resid) r4 = *reinterpret_cast<const uint4*>(p.resid + r * p.ldr + col0 + 8 * j);
+              const uint32_t b[4] = {b4.x, b4.y, b4.z, b4.w}, w[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t sh = e & 1 ? 0 : 16;
+                f[e] = __uint_as_float(v[8 * j + e]);
+                if (p.bias) f[e] += __uint_as_float((b[e >> 1] << sh) & 0xFFFF0000u);
+                if (p.act == WAVE_ACT_GELU_TANH) f[e] = gelu_tanh(f[e]);
+                else if (p.act == WAVE_ACT_GELU_ERF) f[e] = gelu_erf(f[e]);
+                else if (p.act == WAVE_ACT_SILU) f[e] = silu(f[e]);
+                if (p.resid) f[e] += __uint_as_float((w[e >> 1] << sh) & 0xFFFF0000u);
+              }
+              *reinterpret_cast<uint4*>(p.y + r * p.ldy + col0 + 8 * j) =
+                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+            }
+          }
+          __syncwarp();  // rows past M skip the store: reconverge before the next tcgen05.ld
+        }
+      } else if (p.mode == MODE_LINEAR) {
         const int64_t r = (int64_t)mt * 128 + row;
         const bool in = r < p.M;
 #pragma unroll 1
@@ -347,28 +392,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
+template <bool BIAS = false>
 int launch_gemm(const GemmParams& prm, int grid, cudaStream_t stream) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    attr_err = cudaFuncSetAttribute(gemm_wide_kernel<BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     GemmCfg::kSmemBytes);
   });
   if (attr_err != cudaSuccess)
     return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
-  gemm_wide_kernel<<<grid, kGemmThreads, GemmCfg::kSmemBytes, stream>>>(prm);
+  gemm_wide_kernel<BIAS><<<grid, kGemmThreads, GemmCfg::kSmemBytes, stream>>>(prm);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "gemm_wide_kernel launch: %s", cudaGetErrorString(e));
   return WAVE_OK;
 }
 
-// Tensor map over a K-major bf16 matrix [rows][k] with a box of 64 x box_rows.
+// Tensor map over a K-major bf16 matrix, `rows` rows of k (ld apart; 0: k) with
+// a box of 64 x box_rows.
 int encode_kmajor(CUtensorMap* map, const void* base, int64_t rows, int64_t k, uint32_t box_rows,
-                  const char* what) {
+                  const char* what, int64_t ld = 0) {
   auto encode = tensor_map_encoder();
   if (!encode) return fail(WAVE_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
   cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)k * 2};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : k) * 2};
   cuuint32_t box[2] = {64, box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
@@ -377,8 +424,6 @@ int encode_kmajor(CUtensorMap* map, const void* base, int64_t rows, int64_t k, u
   if (r != CUDA_SUCCESS) return fail(WAVE_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed: %d", what, (int)r);
   return WAVE_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
 
@@ -486,7 +531,10 @@ extern "C" int wave_qkv_append_round(wave_kv* kv, const wave_node* nodes, int32_
     std::string keep = wave_last_error_detail();
     for (int32_t i = 0; i < taken; ++i) wave_kv_release(kv, nodes[i].chunk, nodes[i].level);
     fail(rc, "%s", keep.c_str());
+    return rc;
   }
+  for (int32_t i = 0; i < n_nodes; ++i)
+    kv->entries.at(std::make_pair(nodes[i].chunk, nodes[i].level)).written = T;
   return rc;
 }
 
@@ -521,4 +569,49 @@ extern "C" int wave_linear(wave_kv* kv, const void* A, int32_t M, int32_t K, con
   prm.y = static_cast<uint16_t*>(Y);
   prm.resid = static_cast<const uint16_t*>(R);
   return launch_gemm(prm, std::min(prm.n_tiles, kv->num_sms), static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int wave_linear_bias(wave_kv* kv, const void* A, int64_t lda, int32_t M, int32_t K,
+                                const void* W, int32_t N, const void* bias, const void* R,
+                                int64_t ldr, int32_t act, void* Y, int64_t ldy, void* stream) {
+  clear_error();
+  if (!kv) return fail(WAVE_ERR_ARG, "NULL handle");
+  if (!kv->on_device) return fail(WAVE_ERR_ARG, "host-only handle (pool == NULL) cannot launch");
+  if (M < 0 || K < 8 || K % 8 != 0 || K > (1 << 16) || N < 8 || N % 8 != 0 || N > (1 << 16))
+    return fail(WAVE_ERR_ARG, "need M >= 0, K and N positive multiples of 8 (at most 65536); got "
+                "M %d, K %d, N %d", M, K, N);
+  if ((int64_t)M * N >= (1LL << 40)) return fail(WAVE_ERR_ARG, "M x N too large");
+  if (act < WAVE_ACT_NONE || act > WAVE_ACT_SILU) return fail(WAVE_ERR_ARG, "unknown activation %d", act);
+  const int64_t most = 1LL << 38;  // the tensor map's stride is below 2^40 bytes
+  if (lda < K || lda % 8 || lda >= most || ldy < N || ldy % 8 || ldy >= most ||
+      (R && (ldr < N || ldr % 8 || ldr >= most)))
+    return fail(WAVE_ERR_ARG, "row strides must be multiples of 8 and cover the row; got lda %lld, "
+                "ldr %lld, ldy %lld", (long long)lda, (long long)ldr, (long long)ldy);
+  if (R && R == Y && ldr != ldy) return fail(WAVE_ERR_ARG, "Y = R needs ldy = ldr");
+  if (M == 0) return WAVE_OK;
+  if (!A || !W || !Y || !aligned16(A) || !aligned16(W) || !aligned16(Y) || (R && !aligned16(R)) ||
+      (bias && !aligned16(bias)))
+    return fail(WAVE_ERR_ARG, "A, W, Y (and bias, R) must be non-NULL and 16-byte aligned");
+  if (int rc = check_current_device(kv)) return rc;
+  static thread_local GemmParams prm;
+  std::memset(&prm, 0, offsetof(GemmParams, pages));
+  if (int rc = encode_kmajor(&prm.tm_a, A, M, K, 128, "A", lda)) return rc;
+  if (int rc = encode_kmajor(&prm.tm_b, W, N, K, 256, "W")) return rc;
+  prm.status = static_cast<int32_t*>(kv->cfg.pool);
+  prm.wait_ns = wait_limit_ns(kv);
+  prm.mode = MODE_LINEAR;
+  prm.k_slices = (K + 63) / 64;  // the tensor maps fill K's tail with zeros
+  prm.n_mtiles = (int)(((int64_t)M + 127) / 128);
+  prm.n_ntiles = (N + 255) / 256;
+  if ((int64_t)prm.n_mtiles * prm.n_ntiles >= (1LL << 30)) return fail(WAVE_ERR_ARG, "M x N too large");
+  prm.n_tiles = prm.n_mtiles * prm.n_ntiles;
+  prm.M = M;
+  prm.N = N;
+  prm.act = act;
+  prm.y = static_cast<uint16_t*>(Y);
+  prm.resid = static_cast<const uint16_t*>(R);
+  prm.bias = static_cast<const uint16_t*>(bias);
+  prm.ldr = ldr;
+  prm.ldy = ldy;
+  return launch_gemm<true>(prm, std::min(prm.n_tiles, kv->num_sms), static_cast<cudaStream_t>(stream));
 }

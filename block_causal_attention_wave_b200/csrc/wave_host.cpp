@@ -315,7 +315,10 @@ int wave_kv_append_batch(wave_kv* kv, int32_t n_entries, const wave_node* entrie
     for (int32_t i = 0; i < n_entries; ++i)
       wave_kv_release(kv, entries[i].chunk, entries[i].level);
     g_detail = keep;
+    return rc;
   }
+  for (int32_t i = 0; i < n_entries; ++i)
+    kv->entries.at(std::make_pair(entries[i].chunk, entries[i].level)).written = ntokens[i];
   return rc;
 }
 

@@ -16,6 +16,7 @@
 struct wave_entry {
   std::vector<int32_t> pages;  // page ids in token order
   int32_t ntokens = 0;
+  int32_t written = 0;  // tokens counted as written, from token 0 on
 };
 
 struct wave_kv {
@@ -32,6 +33,9 @@ struct wave_kv {
   bool fp8 = false;         // pages hold E4M3 codes with per-(page, head) scales
   int64_t scale_offset = 0; // FP8: byte offset of the scale table in the pool
   alignas(64) CUtensorMap tm_kv;  // rows of d bf16 over every page's K and V
+                                  // (FP8 pools: rows of 128 codes, box 128 x d)
+  std::vector<int64_t> page_mark;  // wave_token_attn's host scratch: per page, where
+  int64_t mark_gen = 0;            // the list being built has it (see there)
 };
 
 namespace wavei {
@@ -58,6 +62,11 @@ int build_rows(const wave_kv* kv, const wave_node* active, int n, int policy,
 
 // Validate one query node against the handle's shape.
 int check_query_node(const wave_kv* kv, wave_node node);
+
+// Host memory ran out inside a C entry (the only exception the library's own
+// code can meet).
+inline int no_host_memory() { return fail(WAVE_ERR_CAPACITY, "out of host memory"); }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Device halves (defined in .cu files).
 int device_init(wave_kv* kv);

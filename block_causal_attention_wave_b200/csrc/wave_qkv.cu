@@ -286,6 +286,8 @@ extern "C" int wave_qkv_append(wave_kv* kv, int32_t chunk, int32_t level, const 
     std::string keep = wave_last_error_detail();
     wave_kv_release(kv, chunk, level);
     fail(rc, "%s", keep.c_str());
+    return rc;
   }
+  kv->entries.at(std::make_pair(chunk, level)).written = ntokens;
   return rc;
 }

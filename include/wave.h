@@ -232,6 +232,71 @@ int wave_qkv_append_round(wave_kv* kv, const wave_node* nodes, int32_t n_nodes, 
 int wave_linear(wave_kv* kv, const void* A, int32_t M, int32_t K, const void* W, int32_t N,
                 const void* R, int32_t act, void* Y, void* stream);
 
+/* Activations of wave_linear_bias besides the two above (wave_linear refuses
+ * them). */
+#define WAVE_ACT_GELU_ERF  2 /* 0.5 x (1 + erf(x / sqrt 2)) */
+#define WAVE_ACT_SILU      3 /* x / (1 + e^-x) */
+
+/* A dense layer with a bias, for any number of rows from one token up:
+ * Y = act(A W^T + bias) (+ R), fp32 accumulation and epilogue, one rounding
+ * to bf16. wave_linear is the form without bias for whole rounds; this one
+ * serves blocks whose projections carry a bias, widths that fill no tile, and
+ * the single tokens that stream beside a round ([WS] "streaming unit").
+ * A: device bf16, M rows of K, row stride lda; W: device bf16 [N][K],
+ * contiguous (a linear layer's [out][in] weight); bias: device bf16 [N] or
+ * NULL; R: device bf16, M rows of N, row stride ldr, or NULL (added after
+ * act); Y: device bf16, M rows of N, row stride ldy, written. Columns of Y
+ * past N are not touched. Y may be R itself (with ldy = ldr); Y may overlap
+ * nothing else. Strides are in elements, multiples of 8 and at least the row's
+ * length; all pointers are 16-byte aligned; K and N are multiples of 8, K >= 8,
+ * N >= 8, K, N <= 65536. M = 0 is allowed and does nothing. `kv` as for
+ * wave_linear. Results do not depend on M's other rows, but a row's last bits
+ * may differ between small and large M (the sums are split differently).
+ * Errors: ARG, CUDA. A device-side timeout is reported by wave_kv_status. */
+int wave_linear_bias(wave_kv* kv, const void* A, int64_t lda, int32_t M, int32_t K, const void* W,
+                     int32_t N, const void* bias, const void* R, int64_t ldr, int32_t act,
+                     void* Y, int64_t ldy, void* stream);
+
+#define WAVE_ROTARY_INTERLEAVED 0 /* pair p is elements 2p, 2p + 1               */
+#define WAVE_ROTARY_HALVES      1 /* pair p is elements p, p + d/2               */
+#define WAVE_ROTARY_PER_AXIS    0 /* pair i of an axis with n pairs: base^(-i/n) */
+#define WAVE_ROTARY_LADDER      1 /* pair p of the head: base^(-p / (d/2))       */
+
+/* Rotary embedding over three position axes (frame, row, column; or whatever
+ * the three integers of a token mean). Of a head's d/2 pairs the first
+ * pairs[0] turn with axis 0, the next pairs[1] with axis 1, the next pairs[2]
+ * with axis 2; pairs left over are copied. pairs {d/2 - 2 (d/6), d/6, d/6}
+ * with PER_AXIS and INTERLEAVED is the rotation of wave_rope. */
+typedef struct {
+  int32_t pairs[3]; /* >= 0 each, together at most d/2                         */
+  float base;       /* frequency base, > 1 and finite                          */
+  int32_t layout;   /* WAVE_ROTARY_INTERLEAVED or WAVE_ROTARY_HALVES           */
+  int32_t ladder;   /* WAVE_ROTARY_PER_AXIS or WAVE_ROTARY_LADDER              */
+  int32_t inverse;  /* 1: turn by minus the angle, which is also the gradient
+                       of the forward rotation; 0: forward                     */
+} wave_rotary_spec;
+
+/* Turn the heads of Q, and of K if it is not NULL, of `rows` tokens by their
+ * positions: (a, b) -> (a cos t - b sin t, a sin t + b cos t) with
+ * t = position[axis] * frequency. wave_qkv_append_round fuses the same
+ * rotation for whole chunks of a bf16 pool with head_dim 128; this call serves
+ * every other case: tokens at positions of their own (single tokens, images
+ * and text between the chunks), head_dim 64, an FP8 pool (rotate, then
+ * append), a projection with bias, and gradients.
+ * positions: device int32 [rows][3], any int32 values (angles are reduced
+ * exactly, so far positions lose nothing); Q: device bf16, rows of
+ * [q_heads][d], row stride ldq; Qout: the same shape, row stride ldqo,
+ * written; K, Kout likewise with k_heads. d is the handle's head_dim. Qout may
+ * be Q (with ldqo = ldq) and Kout may be K; otherwise outputs overlap nothing.
+ * Strides in elements, multiples of 8, at least the row's length; 16-byte
+ * aligned pointers (positions: 4). rows = 0 does nothing. Arithmetic is fp32,
+ * one rounding to bf16. The pool itself is not touched; `kv` as for
+ * wave_linear. Errors: ARG, CUDA. */
+int wave_rotary(wave_kv* kv, const wave_rotary_spec* spec, const int32_t* positions, int32_t rows,
+                const void* Q, int64_t ldq, int32_t q_heads, void* Qout, int64_t ldqo,
+                const void* K, int64_t ldk, int32_t k_heads, void* Kout, int64_t ldko,
+                void* stream);
+
 /* Return the pages of (chunk, level) to the free set. Host only; the caller
  * must not release an entry that queued device work still reads (all library
  * kernels read the pool in stream order, so releasing after enqueueing the
@@ -248,6 +313,35 @@ int wave_kv_entry_pages(const wave_kv* kv, int32_t chunk, int32_t level, int32_t
 
 /* Number of free pages. */
 int wave_kv_free_pages(const wave_kv* kv, int32_t* n);
+
+/* Write tokens first[i] .. first[i] + ntokens[i] - 1 of the entries listed,
+ * which wave_kv_alloc (or an append) has given their pages: the cache write of
+ * tokens that arrive one by one or a few at a time, where wave_kv_append
+ * takes an entry whole. K and V: device bf16, one row of [H][d] per token, the
+ * entries' tokens one after another in list order, row strides ldk and ldv (so
+ * the K and V columns of a packed projection are read in place).
+ * An entry fills from its first token on: the library counts the tokens
+ * written so far, first[i] may be at most that count (a rewrite lies below
+ * it), and first[i] + ntokens[i] at most the entry's tokens. An append or a
+ * fused projection counts as having written the entry whole; pages filled by
+ * other means (Wave Parallelism's receiver) are not counted. Rows of a page past
+ * the tokens written are zero after the first write into the page, so an entry
+ * written in pieces has the bytes of one appended whole (bf16).
+ * FP8 pools: a page's scale only grows. With a = the largest magnitude among
+ * the new rows of the page and head, s' = a / 448 if the page holds no other
+ * token with a non-zero value (1 if a = 0), else max(s, a / 448); kept tokens
+ * become E4M3(code * s / s') and new ones E4M3(x / s'), each operation a
+ * float32 one rounded to nearest, E4M3 as for WAVE_KV_FP8_E4M3. So values
+ * already cached may be rounded once more whenever a larger token arrives.
+ * One launch for all entries. `entries`, `first`, `ntokens` are host arrays;
+ * an entry is named once per call. ntokens[i] = 0 writes nothing. Strides in
+ * elements, multiples of 8, >= H * d; 16-byte aligned pointers. Limits:
+ * n_entries <= WAVE_MAX_APPEND_ENTRIES, touched pages <= WAVE_MAX_APPEND_PAGES
+ * in all (CAPACITY). Errors: ARG, MISSING_KV (an entry without pages), CAPACITY,
+ * CUDA; on any error nothing is written or counted. */
+int wave_kv_write_tokens(wave_kv* kv, int32_t n_entries, const wave_node* entries,
+                         const int32_t* first, const int32_t* ntokens, const void* K, int64_t ldk,
+                         const void* V, int64_t ldv, void* stream);
 
 /* The key list of each active node, as the attention kernel reads it: for node
  * i, rows node_offsets[i] .. node_offsets[i+1]-1 of `rows`, each row a pair
@@ -308,6 +402,50 @@ int wave_round_attn_split(wave_kv* kv, const wave_node* active, int32_t n_active
 int wave_round_attn_split_workspace(wave_kv* kv, const wave_node* active, int32_t n_active,
                                     int32_t policy, int32_t splits, uint64_t* bytes,
                                     int32_t* splits_used);
+
+/* Attention of single tokens over the cache: one query token for each listed
+ * node, over the node's key list as wave_gather_table gives it, the own entry
+ * up to own_tokens[i] tokens -- the step of a token that streams into a unit
+ * while it is being written ([WS] "streaming unit", "K/V cache"), where
+ * wave_round_attn takes a chunk's queries whole. For query i, query head x and
+ * its K/V head h = x / (q_heads / H):
+ *   O_i[x] = softmax_k(Q_i[x] . K[k, h] / sqrt(d)) V[k, h]
+ * own_tokens: host int32 [n_active], 0 <= own_tokens[i] <= the entry's tokens,
+ * or NULL for whole entries; with own_tokens[i] = 0 the own entry need not
+ * exist. The tokens counted must have been written (on this stream or before
+ * it). A node may be listed several times (several tokens of one entry, each
+ * with its own count). q_heads: a multiple of H, at most 16 H. A query that sees
+ * no token gets O = 0 and lse = -inf.
+ * Q: device bf16, n_active rows of [q_heads][d], row stride ldq; O likewise with
+ * ldo, written; lse: device float32 [n_active][q_heads], written, or NULL: the
+ * natural logarithm of the sum of exp(score) over the tokens seen, from which
+ * results over parts of a cache can be joined. Strides in elements, multiples
+ * of 8, >= q_heads * d; 16-byte aligned pointers (lse: 4). O overlaps nothing.
+ * bf16 and FP8 pools: an FP8 page is read in place, its values code * s in
+ * float32 without the rounding to bf16 of wave_round_attn_split.
+ * The key lists are cut over the GPU's SMs in pages and joined by a second
+ * launch; a page that several queries read is read once for up to 16 / (q_heads
+ * / H) of them that follow one another in the list. Sums run in a fixed order:
+ * equal calls give equal bytes. A query's last bits may depend on the other
+ * queries of the call, through where its list is cut.
+ * workspace: device buffer, 256-byte aligned, of at least
+ * wave_token_attn_workspace bytes for the same arguments (NULL if that is 0);
+ * scratch, not shared by calls whose kernels may overlap. Limits: n_active <=
+ * WAVE_MAX_NODES, WAVE_MAX_TOKEN_PAGES pages in all, a page counted once per 16
+ * / (q_heads / H) consecutive queries and once per different count of its
+ * tokens (CAPACITY). n_active = 0 does nothing. Errors: ARG, MISSING_KV,
+ * CAPACITY, CUDA. A device-side timeout is reported by wave_kv_status. */
+#define WAVE_MAX_TOKEN_PAGES 5120
+int wave_token_attn(wave_kv* kv, const wave_node* active, int32_t n_active, int32_t policy,
+                    const int32_t* own_tokens, int32_t q_heads, const void* Q, int64_t ldq,
+                    void* O, int64_t ldo, float* lse, void* workspace, uint64_t workspace_bytes,
+                    void* stream);
+
+/* Workspace bytes wave_token_attn needs for these arguments (0: none). Host
+ * only. Errors: as wave_token_attn's checks of them. */
+int wave_token_attn_workspace(wave_kv* kv, const wave_node* active, int32_t n_active,
+                              int32_t policy, const int32_t* own_tokens, int32_t q_heads,
+                              uint64_t* bytes);
 
 /* wave_round_attn without per-call scratch from the caller. The pages have no
  * counterpart to this call; it exists for callers that cannot allocate device
