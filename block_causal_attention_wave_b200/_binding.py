@@ -288,6 +288,7 @@ class KVCache:
     def __init__(self, heads, head_dim, tokens_per_chunk, num_levels, window=0,
                  prefix_tokens=0, pool=None, pool_bytes=None, kv_format=0):
         self.lib = load()
+        self._index = None  # the pool's device, once a call has asked (_device)
         self.heads, self.head_dim = heads, head_dim
         self.tokens, self.levels = tokens_per_chunk, num_levels
         self.window, self.prefix_tokens = window, prefix_tokens
@@ -389,34 +390,47 @@ class KVCache:
                                     _stream_handle(stream)))
         return Y
 
-    def _rows(self, t, what, rows, width, dtype="torch.bfloat16"):
+    def _rows(self, t, what, rows, width, dtype=None):
         """(address, row stride) of a CUDA tensor read as ``rows`` rows of
         ``width`` contiguous elements: 2-D [rows][width], or [rows][heads][d]
         with contiguous heads. A kernel would read a host tensor's address, or
         past a short one, as readily as a good one, so both are refused here."""
-        if str(t.dtype) != dtype or t.device != self.pool.device:
-            raise ValueError(f"{what}: a {dtype} tensor on {self.pool.device} is wanted, got "
-                             f"{t.dtype} on {t.device}")
         shape, stride = t.shape, t.stride()
-        ok = shape[0] == rows and len(shape) in (2, 3) and stride[-1] == 1
-        if len(shape) == 3:
-            ok = ok and shape[1] * shape[2] == width and (shape[1] == 1 or stride[1] == shape[2])
+        n = len(shape)
+        if n == 3:
+            ok = shape[1] * shape[2] == width and (stride[1] == shape[2] or shape[1] == 1)
         else:
-            ok = ok and shape[-1] == width
-        if not ok:
-            raise ValueError(f"{what}: {rows} rows of {width} contiguous elements are wanted, got "
-                             f"shape {tuple(shape)}, strides {tuple(stride)}")
+            ok = n == 2 and shape[1] == width
+        if not (ok and shape[0] == rows and stride[-1] == 1 and t.dtype is (dtype or self._bf16)
+                and t.get_device() == self._index):
+            raise ValueError(f"{what}: {rows} rows of {width} contiguous {dtype or self._bf16} "
+                             f"elements on cuda:{self._index} are wanted, got shape {tuple(shape)}, "
+                             f"strides {tuple(stride)}, {t.dtype} on {t.device}")
         return t.data_ptr(), stride[0] if rows > 1 else width
 
+    def _stream(self, stream):
+        """A cudaStream_t: the given one, or torch's current stream of the pool's
+        device (read without building a Stream object, which costs 3 us)."""
+        if stream is None:
+            return self._current(self._index)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
     def _device(self):
-        if self.pool is None:
-            raise WaveError(ERR_ARG, "host-only handle (pool == NULL)")
+        if self._index is None:
+            if self.pool is None:
+                raise WaveError(ERR_ARG, "host-only handle (pool == NULL)")
+            import torch
+            self._index, self._bf16 = self.pool.get_device(), torch.bfloat16
+            self._f32, self._i32 = torch.float32, torch.int32
+            self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda i: torch.cuda.current_stream(i).cuda_stream)
 
     def linear_bias(self, A, W, Y, bias=None, R=None, act="none", stream=None):
         """Y [M][N] = act(A W^T + bias) (+ R) for A [M][K], W [N][K], bias [N], R
         [M][N]; A, R and Y may have row strides (multiples of 8), Y may be R.
         ``act``: "none", "gelu_tanh", "gelu_erf" or "silu" (or an ACT_* code)."""
-        self._device()
+        if self._index is None:
+            self._device()
         M, K = A.shape
         N = W.shape[0]
         a, lda = self._rows(A, "A", M, K)
@@ -424,11 +438,11 @@ class KVCache:
         y, ldy = self._rows(Y, "Y", M, N)
         if N > 1 and ldw != K:
             raise ValueError("W must be contiguous")
-        b = self._rows(bias.view(1, -1), "bias", 1, N)[0] if bias is not None else None
+        b = self._rows(bias.unsqueeze(0), "bias", 1, N)[0] if bias is not None else None
         r, ldr = self._rows(R, "R", M, N) if R is not None else (None, 0)
         code = ACTIVATIONS[act] if isinstance(act, str) else int(act)
         _check(self.lib.wave_linear_bias(self.h, a, lda, M, K, w, N, b, r, ldr, code, y, ldy,
-                                         _stream_handle(stream)))
+                                         self._stream(stream)))
         return Y
 
     def rotary(self, positions, Q, K=None, Qout=None, Kout=None, pairs=None, base=10000.0,
@@ -439,7 +453,8 @@ class KVCache:
         ``layout``: "interleaved" or "halves"; ``ladder``: "axis" (each axis
         its own frequencies) or "ladder" (one over the head); ``inverse``:
         turn back, which is the gradient of turning."""
-        self._device()
+        if self._index is None:
+            self._device()
         rows, d = Q.shape[0], self.head_dim
         if pairs is None:
             pairs = (d // 2 - 2 * (d // 6), d // 6, d // 6)
@@ -449,7 +464,7 @@ class KVCache:
             Qout = Q
         if K is not None and Kout is None:
             Kout = K
-        p, ldp = self._rows(positions, "positions", rows, 3, "torch.int32")
+        p, ldp = self._rows(positions, "positions", rows, 3, self._i32)
         if rows > 1 and ldp != 3:
             raise ValueError("positions must be contiguous")
         qh = Q.shape[1]
@@ -461,17 +476,18 @@ class KVCache:
             kh = K.shape[1]
             k, ldk = self._rows(K, "K", rows, kh * d)
             ko, ldko = self._rows(Kout, "Kout", rows, kh * d)
-        spec = RotarySpec((ctypes.c_int32 * 3)(*pairs), base, ROTARY_LAYOUTS[layout],
-                          ROTARY_LADDERS[ladder], int(bool(inverse)))
+        spec = RotarySpec(tuple(pairs), base, ROTARY_LAYOUTS[layout], ROTARY_LADDERS[ladder],
+                          bool(inverse))
         _check(self.lib.wave_rotary(self.h, ctypes.byref(spec), p, rows, q, ldq, qh, qo, ldqo, k,
-                                    ldk, kh, ko, ldko, _stream_handle(stream)))
+                                    ldk, kh, ko, ldko, self._stream(stream)))
         return (Qout, Kout) if K is not None else Qout
 
     def write_tokens(self, entries, first, K, V, counts=None, stream=None):
         """Write tokens first[i] .. first[i] + counts[i] - 1 of entry i; K and V
         [sum of counts][H][d] hold the entries' tokens one after another
         (``counts``: one each by default). Entries need pages (alloc)."""
-        self._device()
+        if self._index is None:
+            self._device()
         n = len(entries)
         counts = [1] * n if counts is None else counts
         width, rows = self.heads * self.head_dim, sum(counts)
@@ -479,7 +495,7 @@ class KVCache:
         v, ldv = self._rows(V, "V", rows, width)
         _check(self.lib.wave_kv_write_tokens(self.h, n, _nodes(entries), _ints(first, n, "first"),
                                              _ints(counts, n, "counts"), k, ldk, v, ldv,
-                                             _stream_handle(stream)))
+                                             self._stream(stream)))
 
     def token_attn_workspace(self, active, policy, own_tokens=None, q_heads=None) -> int:
         """Workspace bytes that token_attn needs for these arguments (may be 0)."""
@@ -496,7 +512,8 @@ class KVCache:
         its key list, the own entry up to own_tokens[i] tokens (None: whole
         entries); ``lse`` (float32 [n][q_heads]) receives the log-sum-exp;
         ``workspace`` is a CUDA tensor of token_attn_workspace() bytes."""
-        self._device()
+        if self._index is None:
+            self._device()
         n = len(active)
         q_heads = Q.shape[1]
         own = _ints(own_tokens, n, "own_tokens") if own_tokens is not None else None
@@ -504,16 +521,16 @@ class KVCache:
         o, ldo = self._rows(O, "O", n, q_heads * self.head_dim)
         s = None
         if lse is not None:
-            s, lds = self._rows(lse, "lse", n, q_heads, "torch.float32")
+            s, lds = self._rows(lse, "lse", n, q_heads, self._f32)
             if n > 1 and lds != q_heads:
                 raise ValueError("lse must be contiguous")
         ws, nbytes = None, 0
         if workspace is not None:
-            if workspace.device != self.pool.device or not workspace.is_contiguous():
-                raise ValueError(f"workspace: a contiguous tensor on {self.pool.device} is wanted")
+            if workspace.get_device() != self._index or not workspace.is_contiguous():
+                raise ValueError(f"workspace: a contiguous tensor on cuda:{self._index} is wanted")
             ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         _check(self.lib.wave_token_attn(self.h, _nodes(active), n, _policy(policy), own, q_heads, q,
-                                        ldq, o, ldo, s, ws, nbytes, _stream_handle(stream)))
+                                        ldq, o, ldo, s, ws, nbytes, self._stream(stream)))
         return O
 
     def release(self, chunk, level):

@@ -1,0 +1,456 @@
+// The dense layer with bias where the wide GEMM's tiles would leave SMs idle:
+// single tokens, and rows up to a streaming unit.
+//
+// What both kernels compute: Y = act(A W^T + bias) (+ R), as the wide GEMM's
+// form with bias (wave_gemm.cu).
+//
+// token_rows_kernel, up to 16 rows. Every weight is used once or a few times,
+// so the time is that of reading W from HBM, and for small layers that of one
+// trip to memory. No shared-memory ring: a lane loads 16 bytes of a feature's
+// row straight into the register operand of m16n8k16 MMAs (the order of the
+// contracted index is free, so a lane's eight consecutive k serve two MMAs),
+// rows of A likewise. A block takes 8 FT features; its 8 or 16 warps take
+// neighbouring 32-wide chunks of K, and their sums meet in shared memory in a
+// fixed order.
+//
+// split_rows_kernel, more rows. Tiles of 128 rows x NF features on tcgen05, K
+// cut over the CTAs of a cluster (any number up to 8) until the tiles fill the
+// SMs; each CTA streams its share of K through a TMA ring of up to 192 KB,
+// accumulates in TMEM, and the partial tiles are summed through distributed
+// shared memory in rank order: no workspace, no atomics, one launch. 192
+// threads: warp 0 lane 0 TMA, warp 1 lane 0 tcgen05, warps 2..5 the epilogue.
+// Every wait is bounded.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "ptx.cuh"
+#include "wave_dense.cuh"
+#include "wave_internal.h"
+#include "wave_sync.cuh"
+
+using namespace wptx;
+
+namespace wavei {
+namespace {
+
+__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ uint16_t to_bf16(float f) { return (uint16_t)(pack_bf16x2(f, 0.f) & 0xFFFF); }
+
+// ---------------------------------------------------------------- up to 16 rows
+
+struct TokenRowsParams {
+  const uint16_t* a;
+  const uint16_t* w;
+  uint16_t* y;
+  const uint16_t* resid;
+  const uint16_t* bias;
+  int64_t lda, ldr, ldy;
+  int32_t M, K, N;
+};
+
+// 16 bytes, or zeros without a load (predicated, so that a batch of loads stays
+// straight-line code with all of them in flight). Weights pass by L1.
+__device__ __forceinline__ uint4 ld_weights(const uint16_t* p, bool in) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)in));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_rows(const uint16_t* p, bool in) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)in));
+  return v;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// WARPS: warps that share K; FT: n-tiles of 8 features per block; R16: more than 8 rows.
+template <int WARPS, int FT, bool R16, int ACT>
+__global__ void __launch_bounds__(32 * WARPS) token_rows_kernel(const __grid_constant__ TokenRowsParams p) {
+  constexpr int U = FT == 1 ? 4 : 2;  // chunks of K in a batch
+  __shared__ float red[WARPS][16][8 * FT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r8 = lane >> 2, q4 = lane & 3;
+  const int f0 = blockIdx.x * 8 * FT;
+  const uint16_t* wrow[FT];
+  bool win[FT];
+#pragma unroll
+  for (int t = 0; t < FT; ++t) {
+    const int f = f0 + 8 * t + r8;
+    win[t] = f < p.N;
+    wrow[t] = p.w + (int64_t)(win[t] ? f : 0) * p.K + 8 * q4;
+  }
+  const bool in0 = r8 < p.M, in1 = R16 && r8 + 8 < p.M;
+  const uint16_t* a0 = p.a + (in0 ? r8 : 0) * p.lda + 8 * q4;
+  const uint16_t* a1 = p.a + (in1 ? r8 + 8 : 0) * p.lda + 8 * q4;
+  float acc[FT][4] = {};
+  const int chunks = (p.K + 31) >> 5;
+  // Two batches of loads: one in flight while the other goes through the MMAs.
+  uint4 w[2][U][FT], x0[2][U], x1[2][U];
+  auto load = [&](int c0, int at) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (c0 + u * WARPS) * 32;
+      const bool in = k + 8 * q4 < p.K;
+#pragma unroll
+      for (int t = 0; t < FT; ++t) w[at][u][t] = ld_weights(wrow[t] + k, in && win[t]);
+      x0[at][u] = ld_rows(a0 + k, in && in0);
+      x1[at][u] = make_uint4(0, 0, 0, 0);
+      if (R16) x1[at][u] = ld_rows(a1 + k, in && in1);
+    }
+  };
+  auto multiply = [&](int at) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < FT; ++t) {
+        mma_bf16(acc[t], x0[at][u].x, x1[at][u].x, x0[at][u].y, x1[at][u].y, w[at][u][t].x, w[at][u][t].y);
+        mma_bf16(acc[t], x0[at][u].z, x1[at][u].z, x0[at][u].w, x1[at][u].w, w[at][u][t].z, w[at][u][t].w);
+      }
+  };
+  constexpr int kStep = WARPS * U;
+  load(warp, 0);
+#pragma unroll 1
+  for (int c0 = warp; c0 < chunks; c0 += 2 * kStep) {
+    load(c0 + kStep, 1);
+    multiply(0);
+    load(c0 + 2 * kStep, 0);
+    multiply(1);
+  }
+#pragma unroll
+  for (int t = 0; t < FT; ++t) {
+    *reinterpret_cast<float2*>(&red[warp][r8][8 * t + 2 * q4]) = make_float2(acc[t][0], acc[t][1]);
+    if (R16) *reinterpret_cast<float2*>(&red[warp][r8 + 8][8 * t + 2 * q4]) = make_float2(acc[t][2], acc[t][3]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.M * 8 * FT; i += 32 * WARPS) {
+    const int m = i / (8 * FT), f = i - m * 8 * FT;
+    if (f0 + f >= p.N) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) v += red[k][m][f];
+    if (p.bias) v += bf16_value(p.bias[f0 + f]);
+    v = activate<ACT>(v);
+    if (p.resid) v += bf16_value(p.resid[m * p.ldr + f0 + f]);
+    p.y[m * p.ldy + f0 + f] = to_bf16(v);
+  }
+}
+
+template <int WARPS, int FT, bool R16>
+void launch_token_rows(const TokenRowsParams& p, int act, cudaStream_t s) {
+  const unsigned grid = (unsigned)((p.N + 8 * FT - 1) / (8 * FT));
+  switch (act) {
+    case WAVE_ACT_GELU_TANH: token_rows_kernel<WARPS, FT, R16, WAVE_ACT_GELU_TANH><<<grid, 32 * WARPS, 0, s>>>(p); break;
+    case WAVE_ACT_GELU_ERF: token_rows_kernel<WARPS, FT, R16, WAVE_ACT_GELU_ERF><<<grid, 32 * WARPS, 0, s>>>(p); break;
+    case WAVE_ACT_SILU: token_rows_kernel<WARPS, FT, R16, WAVE_ACT_SILU><<<grid, 32 * WARPS, 0, s>>>(p); break;
+    default: token_rows_kernel<WARPS, FT, R16, WAVE_ACT_NONE><<<grid, 32 * WARPS, 0, s>>>(p);
+  }
+}
+
+// ------------------------------------------------------------------- more rows
+constexpr int kSplitThreads = 192;
+
+template <int NF>
+struct SplitCfg {
+  static constexpr int kATile = 128 * 128;  // 128 rows x 64 bf16
+  static constexpr int kStage = kATile + NF * 128;
+  static constexpr int kStages = 196608 / kStage;
+  static constexpr int kBarOff = kStages * kStage;
+  static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kDrain = kAccFull + 1,
+                       kBars = kDrain + 1;
+  static constexpr int kSmemBytes = kBarOff + kBars * 8 + 16 + 1024;
+  // A row of a partial tile: four floats of padding, so that the 16-byte
+  // stores of eight lanes (eight rows) fall into different banks.
+  static constexpr int kPartRow = NF + 4;
+  static_assert(8 * 16 * kPartRow * 4 <= kBarOff && 7 * 19 * kPartRow * 4 <= kBarOff, "partials reuse the ring");
+  // kind::f16: fp32 accumulate, bf16 A and B, both K-major, N = NF, M = 128.
+  static constexpr uint32_t kIdesc =
+      (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NF >> 3) << 17) | ((128u >> 4) << 24);
+};
+
+struct SplitParams {
+  CUtensorMap tm_a;  // A [M][K], box 64 x box_rows
+  CUtensorMap tm_w;  // W [N][K], box 64 x NF
+  int32_t* status;
+  uint64_t wait_ns;
+  int32_t k_slices, n_ftiles, splits, box_rows;
+  int32_t M, N;
+  uint16_t* y;
+  const uint16_t* resid;
+  const uint16_t* bias;
+  int64_t ldr, ldy;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+}
+// act(f + bias) + R of eight columns of one row, stored.
+template <int ACT>
+__device__ __forceinline__ void finish8(const SplitParams& p, int64_t m, int col, float (&f)[8]) {
+  float b[8] = {}, r[8] = {};
+  if (p.bias) load8(p.bias + col, b);
+  if (p.resid) load8(p.resid + m * p.ldr + col, r);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = activate<ACT>(f[e] + b[e]) + r[e];
+  *reinterpret_cast<uint4*>(p.y + m * p.ldy + col) =
+      make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                 pack_bf16x2(f[6], f[7]));
+}
+
+template <int NF, int ACT>
+__global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __grid_constant__ SplitParams p) {
+  using C = SplitCfg<NF>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_addr(smem);
+  auto bar = [&](int i) -> uint32_t { return sb + C::kBarOff + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * C::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 8 * C::kBars + 4);
+  const Ctl ctl{abort_flag, p.status, p.wait_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % p.splits;  // the CTA's rank in its cluster
+  const int tile = blockIdx.x / p.splits;
+  const int mt = tile / p.n_ftiles, ft = tile - mt * p.n_ftiles;
+  const int k0 = (int)((int64_t)rank * p.k_slices / p.splits);
+  const int k1 = (int)((int64_t)(rank + 1) * p.k_slices / p.splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar(C::kFull + s), 1);
+      mbar_init(bar(C::kEmpty + s), 1);
+    }
+    mbar_init(bar(C::kAccFull), 1);
+    mbar_init(bar(C::kDrain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&p.tm_a);
+    prefetch_tmap(&p.tm_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), NF);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int rows = min(128, p.M - mt * 128);   // rows of this tile
+  const int cols = min(NF, p.N - ft * NF);     // columns of this tile, a multiple of 8
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // Rows past box_rows are left as they are: they only reach unused rows.
+      const uint32_t bytes = NF * 128 + p.box_rows * 128;
+      int n = 0;
+      for (int k = k0; k < k1; ++k, ++n) {
+        const int s = n % S;
+        if (n >= S && !wait_bar(bar(C::kEmpty + s), (n / S - 1) & 1, ctl, 0x501)) break;
+        mbar_arrive_expect_tx(bar(C::kFull + s), bytes);
+        tma_load_2d(sb + s * C::kStage + C::kATile, &p.tm_w, k * 64, ft * NF, bar(C::kFull + s));
+        tma_load_2d(sb + s * C::kStage, &p.tm_a, k * 64, mt * 128, bar(C::kFull + s));
+      }
+      // Copies still in flight land before the ring is reused or the CTA exits.
+      for (int k = n > S ? n - S : 0; k < n; ++k) drain_wait(bar(C::kFull + k % S), (k / S) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int n = 0; n < k1 - k0; ++n) {
+        const int s = n % S;
+        if (!wait_bar(bar(C::kFull + s), (n / S) & 1, ctl, 0x502)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a = sb + s * C::kStage;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss(tmem, desc_k(a + kk * 32), desc_k(a + C::kATile + kk * 32), C::kIdesc,
+                 (n | kk) != 0 ? 1u : 0u);
+        tc_commit(bar(C::kEmpty + s));
+      }
+      if (ok) tc_commit(bar(C::kAccFull));
+      // Every MMA issued above completes before TMEM is released.
+      tc_commit(bar(C::kDrain));
+      drain_wait(bar(C::kDrain), 0);
+    }
+  } else {
+    // Thread: row of the tile (TMEM lane; warp w may read lanes 32 (w % 4) ..).
+    __all_sync(0xffffffffu, wait_bar(bar(C::kAccFull), 0, ctl, 0x503));
+    tc_fence_after();
+  }
+  __syncwarp();
+  const int row = (warp & 3) * 32 + lane;
+  const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  if (p.splits == 1) {
+    if (warp >= 2) {
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t v[32];
+        tmem_ld32_wait(trow + c, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (row < rows && c + 8 * j < cols) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * j + e]);
+            finish8<ACT>(p, (int64_t)mt * 128 + row, ft * NF + c + 8 * j, f);
+          }
+        }
+        __syncwarp();  // reconverge before the next tcgen05.ld
+      }
+    }
+  } else {
+    // Sum the cluster's partial tiles: the CTA of rank o gets rows o * per ..
+    // of every CTA's tile, as [source rank][row][kPartRow], in its ring.
+    const int per = (rows + p.splits - 1) / p.splits;
+    cluster_sync();  // every CTA of the cluster is done with its ring
+    if (warp >= 2) {
+      const int owner = row < rows ? row / per : rank;
+      const uint32_t local = sb + (uint32_t)((rank * per + row - owner * per) * C::kPartRow) * 4;
+      uint32_t remote;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(owner));
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t v[32];
+        tmem_ld32_wait(trow + c, v);
+        if (row < rows) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(remote + (uint32_t)(c + 4 * j) * 4),
+                         "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3])
+                         : "memory");
+        }
+        __syncwarp();
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+    const float* part = reinterpret_cast<const float*>(smem);
+    const int mine = min(per, rows - rank * per);  // may be <= 0 for the last ranks
+    const int vec = cols >> 3;
+    for (int i = threadIdx.x; i < mine * vec; i += kSplitThreads) {
+      const int r = i / vec, c = (i - r * vec) * 8;
+      float f[8] = {};
+      for (int s = 0; s < p.splits; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(part + (s * per + r) * C::kPartRow + c);
+        const float4 lo = src[0], hi = src[1];
+        f[0] += lo.x; f[1] += lo.y; f[2] += lo.z; f[3] += lo.w;
+        f[4] += hi.x; f[5] += hi.y; f[6] += hi.z; f[7] += hi.w;
+      }
+      finish8<ACT>(p, (int64_t)mt * 128 + rank * per + r, ft * NF + c, f);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, NF);
+  }
+}
+
+template <int NF, int ACT>
+int launch_split(const SplitParams& p, int tiles, cudaStream_t s) {
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(split_rows_kernel<NF, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    SplitCfg<NF>::kSmemBytes);
+  });
+  if (attr_err != cudaSuccess)
+    return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * p.splits));
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = SplitCfg<NF>::kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)p.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, split_rows_kernel<NF, ACT>, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(WAVE_ERR_CUDA, "split_rows_kernel launch: %s", cudaGetErrorString(e));
+  }
+  return WAVE_OK;
+}
+
+template <int NF>
+int launch_split_act(const SplitParams& p, int tiles, int act, cudaStream_t s) {
+  switch (act) {
+    case WAVE_ACT_GELU_TANH: return launch_split<NF, WAVE_ACT_GELU_TANH>(p, tiles, s);
+    case WAVE_ACT_GELU_ERF: return launch_split<NF, WAVE_ACT_GELU_ERF>(p, tiles, s);
+    case WAVE_ACT_SILU: return launch_split<NF, WAVE_ACT_SILU>(p, tiles, s);
+    default: return launch_split<NF, WAVE_ACT_NONE>(p, tiles, s);
+  }
+}
+
+}  // namespace
+
+int token_rows_launch(const DenseArgs& a, int ft, int warps, cudaStream_t s) {
+  const TokenRowsParams p{static_cast<const uint16_t*>(a.A), static_cast<const uint16_t*>(a.W), a.Y, a.R, a.bias,
+                          a.lda, a.ldr, a.ldy, a.M, a.K, a.N};
+  const bool r16 = a.M > 8;
+  if (warps == 16) {
+    if (ft == 1) r16 ? launch_token_rows<16, 1, true>(p, a.act, s) : launch_token_rows<16, 1, false>(p, a.act, s);
+    else r16 ? launch_token_rows<16, 2, true>(p, a.act, s) : launch_token_rows<16, 2, false>(p, a.act, s);
+  } else {
+    if (ft == 1) r16 ? launch_token_rows<8, 1, true>(p, a.act, s) : launch_token_rows<8, 1, false>(p, a.act, s);
+    else r16 ? launch_token_rows<8, 2, true>(p, a.act, s) : launch_token_rows<8, 2, false>(p, a.act, s);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "token_rows_kernel launch: %s", cudaGetErrorString(e));
+  return WAVE_OK;
+}
+
+int split_rows_launch(const wave_kv* kv, const DenseArgs& a, int nf, int splits, cudaStream_t s) {
+  SplitParams p = {};
+  p.box_rows = std::min(128, (a.M + 15) / 16 * 16);
+  if (int rc = encode_kmajor(&p.tm_w, a.W, a.N, a.K, (uint32_t)nf, "W")) return rc;
+  if (int rc = encode_kmajor(&p.tm_a, a.A, a.M, a.K, (uint32_t)p.box_rows, "A", a.lda)) return rc;
+  p.status = static_cast<int32_t*>(kv->cfg.pool);
+  p.wait_ns = wait_limit_ns(kv);
+  p.k_slices = (a.K + 63) / 64;
+  p.n_ftiles = (a.N + nf - 1) / nf;
+  p.splits = splits;
+  p.M = a.M;
+  p.N = a.N;
+  p.y = a.Y;
+  p.resid = a.R;
+  p.bias = a.bias;
+  p.ldr = a.ldr;
+  p.ldy = a.ldy;
+  const int tiles = p.n_ftiles * ((a.M + 127) / 128);
+  if (nf == 64) return launch_split_act<64>(p, tiles, a.act, s);
+  if (nf == 128) return launch_split_act<128>(p, tiles, a.act, s);
+  return launch_split_act<256>(p, tiles, a.act, s);
+}
+
+}  // namespace wavei

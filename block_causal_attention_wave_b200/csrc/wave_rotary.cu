@@ -203,8 +203,8 @@ extern "C" int wave_rotary(wave_kv* kv, const wave_rotary_spec* spec, const int3
     for (int i = 0; i < n[axis]; ++i, ++pr, freq *= step) {
       // freq / (2 pi), as a 64-bit fraction of a turn; at least one unit, so a
       // pair that turns is told from one that is copied.
-      const long double turns = freq / 6.283185307179586476925286766559L;
-      p.turn[pr] = std::max<uint64_t>(1, (uint64_t)roundl(ldexpl(turns, 64)));
+      constexpr long double kUnits = 18446744073709551616.0L / 6.283185307179586476925286766559L;
+      p.turn[pr] = std::max<uint64_t>(1, (uint64_t)(freq * kUnits + 0.5L));
       p.axis[pr] = (int8_t)axis;
     }
   }

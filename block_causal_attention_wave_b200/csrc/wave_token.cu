@@ -15,14 +15,21 @@
 //   - A list item is a page together with the number of its tokens seen and a
 //     16-bit mask of the query rows that see them; up to 16 query rows
 //     (consecutive queries times g heads) form a group, whose distinct items are
-//     read once. A unit is (group, head, item); the units, in that order, are
-//     cut into equal runs, one per SM, wherever the cut falls. A run's part of
-//     one (group, head) is a segment: a whole (group, head) goes straight to O,
-//     others leave their (m, l, O') in the workspace for the join kernel.
-//   - Warp 8 feeds a ring of K and V tiles by TMA (192 KB in flight per SM).
-//   - Warps 0..7 take 16 of the page's 128 keys each, for all 16 rows, with
-//     their own running maximum, sum and O: no exchange between warps until the
-//     segment ends. S = Q K^T and O += P V are m16n8k16 MMAs on fragments read
+//     read once. A list is a group's items for one K/V head. A cluster of 1 to 8
+//     CTAs takes a list, each CTA an equal run of its items, and joins the parts
+//     through distributed shared memory: one launch, no workspace. An SM draws at
+//     most about 95 GB/s through TMA, so 70 of them already saturate HBM, and
+//     clusters that do not pack all 148 cost nothing. Fewer than 8 long lists
+//     are cut into parts for several clusters each, which leave their (m, l, O')
+//     in the workspace for a second kernel.
+//   - Warps 0..7 are two teams that take every other unit; a warp takes 32 of
+//     the page's 128 keys, for all 16 rows, with its own running maximum, sum
+//     and O: no exchange between warps until the segment ends.
+//   - Warps 8 and 9 feed one team each, K and V tiles by TMA through a ring of
+//     the team's own (192 KB in flight per SM). A ring that both teams shared
+//     would need every warp at every slot: a parity wait tells apart only the
+//     phase after the last one its waiter saw, so a team that skipped the other
+//     team's fill of a slot could take it for its own. S = Q K^T and O += P V are m16n8k16 MMAs on fragments read
 //     from shared memory; one token fills one of 16 rows, but at a byte a cycle
 //     a thread the tensor pipe idles either way, and 16 rows cost what one costs.
 //   - Within an MMA the order of the contracted index is free, so a lane's
@@ -48,6 +55,7 @@
 #include <cstring>
 #include <mutex>
 #include <new>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -60,12 +68,19 @@ using namespace wptx;
 namespace wavei {
 namespace {
 
-constexpr int kTokWarps = 8;                       // consumers, 16 keys each
-constexpr int kTokThreads = 32 * (kTokWarps + 1);  // and a producer warp
+constexpr int kTokWarps = 8;                       // consumers
+constexpr int kTokTeam = 4;                        // warps of a unit, 32 keys each
+constexpr int kTokTeams = kTokWarps / kTokTeam;    // unit n of a CTA goes to team n % 2
+// A warpgroup of producers follows, one warp per team and two idle ones: registers
+// move between whole warpgroups.
+constexpr int kTokThreads = 32 * (kTokWarps + 4);
+// d = 128: 168 registers a thread at launch (64,512 of the SM's) become 72 for the
+// producers and 216 for the consumers, 128 * 72 + 256 * 216 = 64,512.
+constexpr int kTokRegsLaunch = 168, kTokRegsFeed = 72, kTokRegsWork = 216;
+static_assert(128 * kTokRegsFeed + 256 * kTokRegsWork <= kTokThreads * kTokRegsLaunch, "register split");
 constexpr int kTokRows = 16;                       // query rows of a group
 
 struct TokGroup {
-  int32_t unit0;    // first unit of the group
   int32_t item0;    // first item in the tables
   int32_t n_items;
   int32_t q0;       // first query
@@ -78,8 +93,8 @@ struct TokHead {
   const uint16_t* q;
   uint16_t* o;
   float* lse;                // or null
-  float* part_o;             // [slot][rows_max][d]
-  float2* part_ml;           // [slot][rows_max]
+  float* part_o;             // [list][part][rows_max][d]
+  float2* part_ml;           // [list][part][rows_max]
   int64_t ldq, ldo;
   int32_t* status;
   uint64_t wait_ns;
@@ -87,8 +102,8 @@ struct TokHead {
   int32_t heads;             // K/V heads
   int32_t per_kv;            // query heads per K/V head
   int32_t n_groups;
-  int32_t units;
-  int32_t ctas;
+  int32_t cluster;           // CTAs per cluster
+  int32_t parts;             // clusters per list
   int32_t rows_max;
   TokGroup g[WAVE_MAX_NODES];
 };
@@ -106,42 +121,18 @@ static_assert(sizeof(TokParams<WAVE_MAX_TOKEN_PAGES>) <= 32760, "kernel paramete
 template <int D, bool FP8>
 struct TokCfg {
   static constexpr int kTile = 128 * D * (FP8 ? 1 : 2);
-  static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = 196608 / kStage;
-  static constexpr int kRedOff = kStages * kStage;                    // [8][16][32] fp32
-  static constexpr int kStatOff = kRedOff + kTokWarps * kTokRows * 32 * 4;  // [8][16] float2
-  static constexpr int kBarOff = kStatOff + kTokWarps * kTokRows * 8;
-  static constexpr int kSmemBytes = kBarOff + 2 * kStages * 8 + 16 + 1024;
+  static constexpr int kSlots = 98304 / kTile;                        // of each team's ring
+  static constexpr int kStatOff = kTokTeams * kSlots * kTile;         // [8][16] float2
+  static constexpr int kMlOff = kStatOff + kTokWarps * kTokRows * 8;  // [16] float2: the CTA's
+  static constexpr int kBarOff = kMlOff + kTokRows * 8;
+  static constexpr int kSmemBytes = kBarOff + 2 * kTokTeams * kSlots * 8 + 16 + 1024;
+  // After the last tile the ring holds the warps' O, [8][16][kRow] fp32, and
+  // behind it the CTA's, [16][kRow].
+  static constexpr int kRow = D + 4;
+  static constexpr int kCtaOff = kTokWarps * kTokRows * kRow * 4;
+  static_assert(kCtaOff + kTokRows * kRow * 4 <= kStatOff, "the joins reuse the ring");
   static constexpr int kTiles = D / 8;    // n-tiles of O
   static constexpr int kSteps = D / 16;   // k-steps of Q K^T
-};
-
-// First unit of CTA c, and the CTA that holds unit u.
-__host__ __device__ __forceinline__ int tok_first(int c, int units, int ctas) {
-  return (int)((int64_t)c * units / ctas);
-}
-__device__ __forceinline__ int tok_cta(int u, int units, int ctas) {
-  return (int)((((int64_t)u + 1) * ctas - 1) / units);
-}
-
-// Walk over a CTA's units: group, head, item.
-struct TokWalk {
-  int g, head, item;
-  __device__ __forceinline__ void start(const TokHead& p, int u) {
-    g = 0;
-    while (g + 1 < p.n_groups && u >= p.g[g + 1].unit0) ++g;
-    const int local = u - p.g[g].unit0;
-    head = local / p.g[g].n_items;
-    item = local - head * p.g[g].n_items;
-  }
-  __device__ __forceinline__ void next(const TokHead& p) {
-    if (++item < p.g[g].n_items) return;
-    item = 0;
-    if (++head < p.heads) return;
-    head = 0;
-    do ++g;
-    while (g < p.n_groups && p.g[g].n_items == 0);
-  }
 };
 
 template <bool F16>
@@ -180,6 +171,22 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ void tok_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float (pair) at shared address `addr` of the cluster's CTA `rank`.
+__device__ __forceinline__ float lds_rank(uint32_t addr, int rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 lds_rank2(uint32_t addr, int rank) {
+  float2 v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+               : "=f"(v.x), "=f"(v.y) : "r"(addr), "r"(rank) : "memory");
+  return v;
+}
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kTokWarps) : "memory");
 }
@@ -195,94 +202,95 @@ template <int D, bool FP8, int CAP>
 __global__ void __launch_bounds__(kTokThreads, 1)
     token_attn_kernel(const __grid_constant__ TokParams<CAP> p) {
   using C = TokCfg<D, FP8>;
-  constexpr int S = C::kStages;
+  constexpr int S = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_addr(smem);
-  auto full = [&](int s) -> uint32_t { return sb + C::kBarOff + 8u * s; };
-  auto empty = [&](int s) -> uint32_t { return sb + C::kBarOff + 8u * (S + s); };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 16 * S);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 16 * kTokTeams * S);
   const TokHead& h = p.h;
   const Ctl ctl{abort_flag, h.status, h.wait_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int u0 = tok_first(blockIdx.x, h.units, h.ctas);
-  const int u1 = tok_first(blockIdx.x + 1, h.units, h.ctas);
+  // This CTA's list (group, K/V head), part, rank in the cluster, and items.
+  const int rank = blockIdx.x % h.cluster;
+  const int part_id = blockIdx.x / h.cluster % h.parts;
+  const int list = blockIdx.x / (h.cluster * h.parts);
+  const int head = list % h.heads;
+  const TokGroup& grp = h.g[list / h.heads];
+  const int share = part_id * h.cluster + rank, shares = h.cluster * h.parts;
+  const int u0 = (int)((int64_t)grp.n_items * share / shares);
+  const int u1 = (int)((int64_t)grp.n_items * (share + 1) / shares);
+  const uint32_t* pages = p.page + grp.item0;
+  const uint16_t* masks = p.mask + grp.item0;
+  // The ring of this warp's team: fill f (K of the team's unit j is fill 2 j, V
+  // fill 2 j + 1) is in slot f % S, in phase f / S of its barriers.
+  const int team = warp < kTokWarps ? warp / kTokTeam : warp - kTokWarps;
+  const uint32_t ring = sb + team * S * C::kTile;
+  const uint32_t bars = sb + C::kBarOff + 16u * S * team;
+  auto full = [&](int s) -> uint32_t { return bars + 8u * s; };
+  auto empty = [&](int s) -> uint32_t { return bars + 8u * (S + s); };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), kTokWarps);
-    }
+    for (int t = 0; t < kTokTeams; ++t)
+      for (int s = 0; s < S; ++s) {
+        mbar_init(sb + C::kBarOff + 16u * S * t + 8u * s, 1);
+        mbar_init(sb + C::kBarOff + 16u * S * t + 8u * (S + s), kTokTeam);
+      }
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&h.tm);
   }
   __syncthreads();
-  if (u0 >= u1) return;
 
-  if (warp == kTokWarps) {
-    if (lane == 0) {
-      TokWalk w;
-      w.start(h, u0);
-      int n = 0;
-      for (int u = u0; u < u1; ++u, ++n, w.next(h)) {
-        const int s = n % S;
-        if (n >= S && !wait_bar(empty(s), (n / S - 1) & 1, ctl, 0x401)) break;
-        const int item = h.g[w.g].item0 + w.item;
-        const int page = (int)(p.page[item] & 0x1FFFFFFu);
-        const uint32_t dst = sb + s * C::kStage;
-        mbar_arrive_expect_tx(full(s), C::kStage);
+  if (warp >= kTokWarps) {
+    if constexpr (D == 128) regs_dec<kTokRegsFeed>();
+    if (lane == 0 && team < kTokTeams) {
+      int f = 0;
+      bool ok = true;
+      for (int u = u0 + team; u < u1 && ok; u += kTokTeams) {
+        const int page = (int)(pages[u] & 0x1FFFFFFu);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const int tile = (page * 2 + kv) * h.heads + w.head;
+          const int s = f % S;
+          if (f >= S && !wait_bar(empty(s), (f / S - 1) & 1, ctl, 0x401)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = ring + s * C::kTile;
+          const int tile = (page * 2 + kv) * h.heads + head;
+          mbar_arrive_expect_tx(full(s), C::kTile);
           if constexpr (FP8) {
-            tma_load_2d(dst + kv * C::kTile, &h.tm, 0, tile * D, full(s));
+            tma_load_2d(dst, &h.tm, 0, tile * D, full(s));
           } else {
 #pragma unroll
-            for (int b = 0; b < D / 64; ++b)
-              tma_load_2d(dst + kv * C::kTile + b * 16384, &h.tm, 64 * b, tile * 128, full(s));
+            for (int b = 0; b < D / 64; ++b) tma_load_2d(dst + b * 16384, &h.tm, 64 * b, tile * 128, full(s));
           }
+          ++f;
         }
       }
       // Copies still in flight land before the CTA exits.
-      for (int k = n > S ? n - S : 0; k < n; ++k) drain_wait(full(k % S), (k / S) & 1);
+      for (int k = f > S ? f - S : 0; k < f; ++k) drain_wait(full(k % S), (k / S) & 1);
     }
+    // These warps end here (the cluster's barriers wait for threads that have not
+    // exited): what follows may use more registers than they kept.
     return;
   }
-
-  // ---- consumers: keys 16 warp .. 16 warp + 15 of every page
+  if constexpr (D == 128) regs_inc<kTokRegsWork>();
+  {
+  // ---- consumers: keys 32 (warp % 4) .. + 31 of every other page
+  const int key0 = 32 * (warp % kTokTeam);
   const int r8 = lane >> 2, q4 = lane & 3;   // fragment row (and column group), lane quarter
   float o[C::kTiles][4];
   uint32_t qa[C::kSteps][4];
   float m[2], l[2], qs[2];   // rows r8 and r8 + 8: maximum (log2), this lane's sum, score factor
-  float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
-  float* red = reinterpret_cast<float*>(smem + C::kRedOff);
   bool dead = false;
-  TokWalk w;
-  w.start(h, u0);
-  float next_sk = 0.f, next_sv = 0.f;
-  auto fetch_scales = [&](const TokWalk& at) {
-    if constexpr (FP8) {
-      const int64_t page = p.page[h.g[at.g].item0 + at.item] & 0x1FFFFFFu;
-      next_sk = __ldg(h.scales + (page * 2) * h.heads + at.head);
-      next_sv = __ldg(h.scales + (page * 2 + 1) * h.heads + at.head);
-    }
-  };
-  fetch_scales(w);
-  int n = 0;
-  for (int u = u0; u < u1;) {
-    // ---- a segment: units of one (group, head)
-    const TokGroup& grp = h.g[w.g];
-    const int seg_head = w.head, seg_g = w.g;
-    const int seg_end = min(u1, u + grp.n_items - w.item);
-    const int rows = grp.rows;
-    const uint32_t all_rows = (1u << rows) - 1;
+  const int rows = grp.rows;
+  const uint32_t all_rows = (1u << rows) - 1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = r8 + 8 * i;
       const uint16_t* src = h.q + (grp.q0 + row / h.per_kv) * h.ldq +
-                            (int64_t)(seg_head * h.per_kv + row % h.per_kv) * D;
+                            (int64_t)(head * h.per_kv + row % h.per_kv) * D;
       const bool in = row < rows;
       m[i] = -INFINITY;
       l[i] = 0.f;
@@ -342,22 +350,19 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[t][c] = 0.f;
 
-    for (; u < seg_end; ++u, ++n) {
-      const int s = n % S;
-      const int item = grp.item0 + w.item;
-      const int seen = (int)(p.page[item] >> 25) + 1;
-      const uint32_t mask = p.mask[item];
-      const float sk = next_sk, sv = next_sv;
-      w.next(h);
-      if (FP8 && u + 1 < u1) fetch_scales(w);
-      if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(full(s), (n / S) & 1, ctl, 0x402));
-      if (dead) continue;
-      const int key0 = 16 * warp;
-      if (key0 < seen) {
-        const uint32_t kt = sb + s * C::kStage, vt = kt + C::kTile;
-        float sc[2][4];
+    // One unit: S = Q K^T, the softmax's step, O += P V, for the warp's 32 keys.
+    // false: a wait ran out. WHOLE: every row sees all 128 tokens.
+    auto unit = [&](auto whole_c, int ks, int vs, int vp, int seen, uint32_t mask, float sk, float sv) -> bool {
+      constexpr bool WHOLE = decltype(whole_c)::value;
+      const bool some = WHOLE || key0 < seen;   // the warp has a key that is seen
+      uint32_t pa[2][4];               // P of the warp's two blocks of sixteen keys
+      const bool part[2] = {(mask >> r8 & 1) != 0, (mask >> (r8 + 8) & 1) != 0};
+      if (some) {
+        const uint32_t kt = ring + ks * C::kTile;
+        // ---- S = Q K^T, n-tiles of 8 keys
+        float sc[4][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
         if constexpr (!FP8) {
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt) {
+              for (int nt = 0; nt < 4; ++nt) {
                 const uint32_t row = kt + b * 16384 + (key0 + nt * 8 + r8) * 128;
                 const uint4 v = lds128(row + (((2 * q4 + hh) ^ r8) << 4));
                 const int st = (b * 2 + hh) * 2;
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 #pragma unroll
           for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < 4; ++nt) {
               const int key = key0 + nt * 8 + r8;
               const int line = D == 128 ? key : key >> 1;
               const int chunk = D == 128 ? 2 * q4 + hh : (key & 1) * 4 + q4;
@@ -388,22 +393,25 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 tok_mma<true>(sc[nt], qa[hh * 4 + j], e4m3_f16x2(wd[j] & 0xFFFF), e4m3_f16x2(wd[j] >> 16));
             }
         }
-        // ---- softmax of this warp's 16 keys; rows r8 (c = 0, 1) and r8 + 8 (c = 2, 3)
-        const bool part[2] = {(mask >> r8 & 1) != 0, (mask >> (r8 + 8) & 1) != 0};
-        float top[2] = {-INFINITY, -INFINITY};
+        // ---- softmax of this warp's keys; rows r8 (c = 0, 1) and r8 + 8 (c = 2, 3)
+        float top[2] = {-INFINITY, -INFINITY}, shift[2];
+        const float f0 = FP8 ? qs[0] * sk : qs[0], f1 = FP8 ? qs[1] * sk : qs[1];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = key0 + nt * 8 + 2 * q4 + (c & 1);
-            const float f = FP8 ? qs[c >> 1] * sk : qs[c >> 1];
-            sc[nt][c] = part[c >> 1] && key < seen ? sc[nt][c] * f : -INFINITY;
-            top[c >> 1] = fmaxf(top[c >> 1], sc[nt][c]);
-          }
+          for (int c = 0; c < 4; ++c) sc[nt][c] *= c < 2 ? f0 : f1;
+        if (!WHOLE) {
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (!part[c >> 1] || key0 + nt * 8 + 2 * q4 + (c & 1) >= seen) sc[nt][c] = -INFINITY;
+        }
         bool grew = false;
-        float shift[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) top[i] = fmax3(top[i], sc[nt][2 * i], sc[nt][2 * i + 1]);
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
           top[i] = fmaxf(top[i], m[i]);
@@ -413,8 +421,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float f = ex2_approx(m[i] - shift[i]);
             if (top[i] > m[i]) {
+              const float f = ex2_approx(m[i] - shift[i]);
               l[i] *= f;
               m[i] = top[i];
 #pragma unroll
@@ -425,94 +433,128 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             }
           }
         }
-        uint32_t pa[4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float a = ex2_approx(sc[nt][2 * i] - shift[i]);
             const float b = ex2_approx(sc[nt][2 * i + 1] - shift[i]);
             l[i] += a + b;
-            pa[2 * nt + i] = FP8 ? pack_f16x2(a * 32768.f, b * 32768.f) : pack_bf16x2(a, b);
+            pa[nt >> 1][2 * (nt & 1) + i] = FP8 ? pack_f16x2(a * 32768.f, b * 32768.f) : pack_bf16x2(a, b);
           }
-        // ---- O += P V: keys 2 q4, + 1, + 8, + 9 of the warp's sixteen
-        const bool partial = seen < key0 + 16;
-        const bool mixed = (mask & all_rows) != all_rows;
-        bool live[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) live[k] = key0 + 2 * q4 + (k & 1) + 8 * (k >> 1) < seen;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(ks));
+      if (!__all_sync(0xffffffffu, wait_bar(full(vs), vp, ctl, 0x403))) return false;
+      if (some) {
+        // ---- O += P V: of each block, a lane's keys are 2 q4, + 1, + 8, + 9
+        const uint32_t vt = ring + vs * C::kTile;
+        auto key_of = [&](int kb, int k) { return key0 + 16 * kb + 2 * q4 + (k & 1) + 8 * (k >> 1); };
         if constexpr (!FP8) {
 #pragma unroll
-          for (int b = 0; b < D / 64; ++b) {
-            uint4 v[4];
+          for (int b = 0; b < D / 64; ++b)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int key = key0 + 2 * q4 + (k & 1) + 8 * (k >> 1);
-              v[k] = lds128(vt + b * 16384 + key * 128 + ((r8 ^ (key & 7)) << 4));
-              if (partial && !live[k]) v[k] = make_uint4(0, 0, 0, 0);
-            }
-            const uint32_t x[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
-                                      {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
+            for (int kb = 0; kb < 2; ++kb) {
+              uint32_t x[4][4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
-              const uint32_t b0 = __byte_perm(x[0][e >> 1], x[1][e >> 1], sel);
-              const uint32_t b1 = __byte_perm(x[2][e >> 1], x[3][e >> 1], sel);
-              float (&acc)[4] = o[b * 8 + e];
-              if (!mixed) {
-                tok_mma<false>(acc, pa, b0, b1);
-              } else {
-                float d[4] = {acc[0], acc[1], acc[2], acc[3]};
-                tok_mma<false>(d, pa, b0, b1);
+              for (int k = 0; k < 4; ++k) {
+                const int key = key_of(kb, k);
+                uint4 v = lds128(vt + b * 16384 + key * 128 + ((r8 ^ (key & 7)) << 4));
+                if (!WHOLE && key >= seen) v = make_uint4(0, 0, 0, 0);
+                x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
+              }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[c] = part[c >> 1] ? d[c] : acc[c];
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
+                const uint32_t b0 = __byte_perm(x[0][e >> 1], x[1][e >> 1], sel);
+                const uint32_t b1 = __byte_perm(x[2][e >> 1], x[3][e >> 1], sel);
+                float (&acc)[4] = o[b * 8 + e];
+                if (WHOLE) {
+                  tok_mma<false>(acc, pa[kb], b0, b1);
+                } else {
+                  float d[4] = {acc[0], acc[1], acc[2], acc[3]};
+                  tok_mma<false>(d, pa[kb], b0, b1);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) acc[c] = part[c >> 1] ? d[c] : acc[c];
+                }
               }
             }
-          }
         } else {
           const float f = sv * 0x1p-15f;
-          uint32_t x[4][D / 32];
+          uint32_t x[2][4][D / 32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int key = key0 + 2 * q4 + (k & 1) + 8 * (k >> 1);
-            if constexpr (D == 128) {
-              const uint4 v = lds128(vt + key * 128 + ((r8 ^ (key & 7)) << 4));
-              x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
-            } else {
-              const int line = key >> 1, chunk = (key & 1) * 4 + (r8 >> 1);
-              const uint2 v = lds64(vt + line * 128 + ((chunk ^ (line & 7)) << 4) + (r8 & 1) * 8);
-              x[k][0] = v.x; x[k][1] = v.y;
-            }
-            if (partial && !live[k]) {
+          for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-              for (int j = 0; j < D / 32; ++j) x[k][j] = 0;
+            for (int k = 0; k < 4; ++k) {
+              const int key = key_of(kb, k);
+              if constexpr (D == 128) {
+                const uint4 v = lds128(vt + key * 128 + ((r8 ^ (key & 7)) << 4));
+                x[kb][k][0] = v.x; x[kb][k][1] = v.y; x[kb][k][2] = v.z; x[kb][k][3] = v.w;
+              } else {
+                const int line = key >> 1, chunk = (key & 1) * 4 + (r8 >> 1);
+                const uint2 v = lds64(vt + line * 128 + ((chunk ^ (line & 7)) << 4) + (r8 & 1) * 8);
+                x[kb][k][0] = v.x; x[kb][k][1] = v.y;
+              }
+              if (!WHOLE && key >= seen) {
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) x[kb][k][j] = 0;
+              }
             }
-          }
 #pragma unroll
           for (int j = 0; j < D / 32; ++j)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               // codes of d 4 j + 2 half (low 16 bits) and the next: keys (0, 1) and (8, 9)
               const uint32_t sel = half ? 0x7362 : 0x5140;
-              const uint32_t k01 = __byte_perm(x[0][j], x[1][j], sel);
-              const uint32_t k89 = __byte_perm(x[2][j], x[3][j], sel);
+              float d[2][4] = {};
+#pragma unroll
+              for (int kb = 0; kb < 2; ++kb) {
+                const uint32_t k01 = __byte_perm(x[kb][0][j], x[kb][1][j], sel);
+                const uint32_t k89 = __byte_perm(x[kb][2][j], x[kb][3][j], sel);
+                tok_mma<true>(d[0], pa[kb], e4m3_f16x2(k01 & 0xFFFF), e4m3_f16x2(k89 & 0xFFFF));
+                tok_mma<true>(d[1], pa[kb], e4m3_f16x2(k01 >> 16), e4m3_f16x2(k89 >> 16));
+              }
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                tok_mma<true>(d, pa, e4m3_f16x2(e ? k01 >> 16 : k01 & 0xFFFF),
-                              e4m3_f16x2(e ? k89 >> 16 : k89 & 0xFFFF));
                 float (&acc)[4] = o[4 * j + 2 * half + e];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[c] = part[c >> 1] ? fmaf(f, d[c], acc[c]) : acc[c];
+                for (int c = 0; c < 4; ++c)
+                  if (WHOLE || part[c >> 1]) acc[c] = fmaf(f, d[e][c], acc[c]);
               }
             }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
+      if (lane == 0) mbar_arrive(empty(vs));
+      return true;
+    };
+    int f = 0;   // the team's fills taken
+    for (int u = u0 + team; u < u1; u += kTokTeams) {
+      const int ks = f % S, kp = (f / S) & 1, vs = (f + 1) % S, vp = ((f + 1) / S) & 1;
+      f += 2;
+      const int seen = (int)(pages[u] >> 25) + 1;
+      const uint32_t mask = masks[u];
+      float sk = 1.f, sv = 1.f;
+      if constexpr (FP8) {
+        // Two loads that are in flight while the tile is waited for.
+        const int64_t page = pages[u] & 0x1FFFFFFu;
+        sk = __ldg(h.scales + (page * 2) * h.heads + head);
+        sv = __ldg(h.scales + (page * 2 + 1) * h.heads + head);
+      }
+      if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(full(ks), kp, ctl, 0x402));
+      if (dead) continue;
+      // The common unit, of which every row sees every token, has code of its own:
+      // with the selections for the others in line (predicated by the compiler)
+      // a unit took 919 instructions a warp instead of WHOLE_COUNT.
+      const bool whole = seen == kPageTokens && (mask & all_rows) == all_rows;
+      if (whole) dead = !unit(std::true_type{}, ks, vs, vp, seen, mask, sk, sv);
+      else dead = !unit(std::false_type{}, ks, vs, vp, seen, mask, sk, sv);
     }
 
-    // ---- segment end: join the eight warps
+    // ---- join the eight warps: O of each, scaled to the CTA's maximum, goes into
+    // the ring, whose tiles all warps are done with at the first barrier.
+    float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
+    float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -520,75 +562,82 @@ __global__ void __launch_bounds__(kTokThreads, 1)
       if (q4 == 0) stat[warp * kTokRows + r8 + 8 * i] = make_float2(m[i], l[i]);
     }
     consumers_sync();
-    float f[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      const int row = r8 + 8 * i;
+      if (row >= rows) continue;
       float top = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kTokWarps; ++k) top = fmaxf(top, stat[k * kTokRows + r8 + 8 * i].x);
-      f[i] = ex2_approx(m[i] - (top == -INFINITY ? 0.f : top));
-    }
-    const int gh = seg_g * h.heads + seg_head;
-    const int list0 = grp.unit0 + seg_head * grp.n_items;
-    const bool whole = u0 <= list0 && list0 + grp.n_items <= u1;
-    const int64_t slot = (int64_t)(blockIdx.x + gh) * h.rows_max;
-    // 32 columns (4 n-tiles) at a time; thread: row threadIdx.x / 16, columns x, x + 16.
-    const int row = threadIdx.x >> 4;
-    float top = -INFINITY, den = 0.f;
-    if (row < rows) {
-#pragma unroll
       for (int k = 0; k < kTokWarps; ++k) top = fmaxf(top, stat[k * kTokRows + row].x);
+      const float fac = ex2_approx(m[i] - (top == -INFINITY ? 0.f : top));
+      float* dst = red + (warp * kTokRows + row) * C::kRow;
+#pragma unroll
+      for (int t = 0; t < C::kTiles; t += 4)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<float4*>(dst + tok_col<D, FP8>(t, q4, c)) =
+              make_float4(o[t][2 * i + c] * fac, o[t + 1][2 * i + c] * fac, o[t + 2][2 * i + c] * fac,
+                          o[t + 3][2 * i + c] * fac);
+    }
+    consumers_sync();
+    float* cta = reinterpret_cast<float*>(smem + C::kCtaOff);
+    for (int x = threadIdx.x; x < rows * D; x += 32 * kTokWarps) {
+      const int row = x / D, d = x % D;
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kTokWarps; ++k) sum += red[(k * kTokRows + row) * C::kRow + d];
+      cta[row * C::kRow + d] = sum;
+    }
+    if (threadIdx.x < rows) {
+      float top = -INFINITY, den = 0.f;
+#pragma unroll
+      for (int k = 0; k < kTokWarps; ++k) top = fmaxf(top, stat[k * kTokRows + threadIdx.x].x);
 #pragma unroll
       for (int k = 0; k < kTokWarps; ++k) {
-        const float2 ml = stat[k * kTokRows + row];
+        const float2 ml = stat[k * kTokRows + threadIdx.x];
         den += ml.y * ex2_approx(ml.x - (top == -INFINITY ? 0.f : top));
       }
+      reinterpret_cast<float2*>(smem + C::kMlOff)[threadIdx.x] = make_float2(top, den);
     }
-    const int64_t query = grp.q0 + row / h.per_kv;
-    const int qhead = seg_head * h.per_kv + row % h.per_kv;
-    const float inv = top == -INFINITY ? 0.f : 1.f / den;
-#pragma unroll
-    for (int blk = 0; blk < C::kTiles / 4; ++blk) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (r8 + 8 * i >= rows) continue;
-        float* dst = red + (warp * kTokRows + r8 + 8 * i) * 32 + q4 * 8;
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) dst[tt * 2 + c] = o[blk * 4 + tt][2 * i + c] * f[i];
-      }
-      consumers_sync();
-      if (row < rows) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int x = (threadIdx.x & 15) + 16 * j;
-          float sum = 0.f;
-#pragma unroll
-          for (int k = 0; k < kTokWarps; ++k) sum += red[(k * kTokRows + row) * 32 + x];
-          const int d = tok_col<D, FP8>(blk * 4 + ((x >> 1) & 3), x >> 3, x & 1);
-          if (whole) {
-            const float v = top == -INFINITY ? 0.f : sum * inv;
-            h.o[query * h.ldo + (int64_t)qhead * D + d] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFF);
-          } else {
-            h.part_o[(slot + row) * D + d] = sum;
-          }
-        }
-      }
-      consumers_sync();
+  }
+
+  // ---- join the cluster's CTAs, in rank order; rank r finishes every cluster-th
+  // run of columns
+  __syncwarp();
+  if (h.cluster > 1) tok_cluster_sync();
+  else consumers_sync();
+  constexpr int kWorkers = 32 * kTokWarps;
+  for (int x = rank * kWorkers + threadIdx.x; x < grp.rows * D; x += h.cluster * kWorkers) {
+    const int row = x / D, d = x % D;
+    const uint32_t at = sb + C::kCtaOff + (uint32_t)(row * C::kRow + d) * 4, ml_at = sb + C::kMlOff + row * 8;
+    float top = -INFINITY, den = 0.f, sum = 0.f;
+    for (int r = 0; r < h.cluster; ++r) top = fmaxf(top, lds_rank2(ml_at, r).x);
+    const float shift = top == -INFINITY ? 0.f : top;
+    for (int r = 0; r < h.cluster; ++r) {
+      const float2 ml = lds_rank2(ml_at, r);
+      const float e = ex2_approx(ml.x - shift);
+      den += e * ml.y;
+      sum += e * lds_rank(at, r);
     }
-    if (row < rows && (threadIdx.x & 15) == 0) {
-      if (!whole)
-        h.part_ml[slot + row] = make_float2(top, den);
-      else if (h.lse)
+    if (h.parts > 1) {
+      const int64_t slot = (int64_t)(list * h.parts + part_id) * h.rows_max + row;
+      h.part_o[slot * D + d] = sum;
+      if (d == 0) h.part_ml[slot] = make_float2(top, den);
+    } else {
+      const int64_t query = grp.q0 + row / h.per_kv;
+      const int qhead = head * h.per_kv + row % h.per_kv;
+      const float v = top == -INFINITY ? 0.f : sum / den;
+      h.o[query * h.ldo + (int64_t)qhead * D + d] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFF);
+      if (h.lse && d == 0)
         h.lse[query * (h.heads * h.per_kv) + qhead] =
             top == -INFINITY ? -INFINITY : (top + log2f(den)) * 0.6931471805599453f;
     }
   }
+  __syncwarp();
+  if (h.cluster > 1) tok_cluster_sync();  // no CTA leaves while another reads it
 }
 
-// The join: one warp per (query, query head). Lists that one CTA held whole are
-// done already; lists of no item give zeros.
+// The join of a list's parts: one warp per (query, query head).
 constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) token_join_kernel(const __grid_constant__ TokHead h,
@@ -602,34 +651,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) token_join_kernel(const __gri
   const int query = at / q_heads, qhead = at - query * q_heads;
   int g = 0;
   while (g + 1 < h.n_groups && query >= h.g[g + 1].q0) ++g;
-  const TokGroup& grp = h.g[g];
   const int head = qhead / h.per_kv;
-  const int row = (query - grp.q0) * h.per_kv + qhead - head * h.per_kv;
-  uint16_t* dst = h.o + query * h.ldo + (int64_t)qhead * D + lane * V;
-  float acc[V] = {};
-  float mx = -INFINITY, den = 0.f;
-  if (grp.n_items > 0) {
-    const int first = grp.unit0 + head * grp.n_items;
-    const int c0 = tok_cta(first, h.units, h.ctas), c1 = tok_cta(first + grp.n_items - 1, h.units, h.ctas);
-    if (c0 == c1) return;
-    const int64_t base = (int64_t)(g * h.heads + head) * h.rows_max + row;
-    for (int c = c0 + lane; c <= c1; c += 32)
-      mx = fmaxf(mx, h.part_ml[base + (int64_t)c * h.rows_max].x);
+  const int row = (query - h.g[g].q0) * h.per_kv + qhead - head * h.per_kv;
+  const int64_t base = (int64_t)(g * h.heads + head) * h.parts * h.rows_max + row;
+  float mx = -INFINITY, den = 0.f, acc[V] = {};
+  for (int c = 0; c < h.parts; ++c) mx = fmaxf(mx, h.part_ml[base + (int64_t)c * h.rows_max].x);
+  const float shift = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+  for (int c = 0; c < h.parts; ++c) {
+    const int64_t slot = base + (int64_t)c * h.rows_max;
+    const float2 ml = h.part_ml[slot];
+    const float e = ex2_approx(ml.x - shift);
+    den += e * ml.y;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float shift = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t slot = base + (int64_t)c * h.rows_max;
-      const float2 ml = h.part_ml[slot];
-      const float e = exp2f(ml.x - shift);
-      den += e * ml.y;
-      const float* po = h.part_o + slot * D + lane * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += e * po[i];
-    }
+    for (int i = 0; i < V; ++i) acc[i] += e * h.part_o[slot * D + lane * V + i];
   }
   const float inv = mx == -INFINITY ? 0.f : 1.f / den;
+  uint16_t* dst = h.o + query * h.ldo + (int64_t)qhead * D + lane * V;
 #pragma unroll
   for (int i = 0; i < V; i += 2)
     *reinterpret_cast<uint32_t*>(dst + i) =
@@ -643,14 +681,34 @@ int launch_token(const TokParams<CAP>& p, cudaStream_t s) {
   using C = TokCfg<D, FP8>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
+  static int regs = 0;
   std::call_once(once, [] {
     attr_err = cudaFuncSetAttribute(token_attn_kernel<D, FP8, CAP>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    cudaFuncAttributes fa;
+    if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, token_attn_kernel<D, FP8, CAP>);
+    if (attr_err == cudaSuccess) regs = fa.numRegs;
   });
   if (attr_err != cudaSuccess)
     return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
-  token_attn_kernel<D, FP8, CAP><<<p.h.ctas, kTokThreads, C::kSmemBytes, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  // setmaxnreg.inc waits until registers are free: with fewer at launch than the
+  // split assumes it would never return.
+  if (D == 128 && regs < kTokRegsLaunch)
+    return fail(WAVE_ERR_UNSUPPORTED, "token_attn_kernel compiled with %d registers per thread; its "
+                "register split needs %d", regs, kTokRegsLaunch);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.h.n_groups * p.h.heads * p.h.parts * p.h.cluster));
+  cfg.blockDim = dim3(kTokThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)p.h.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.h.cluster > 1 ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, token_attn_kernel<D, FP8, CAP>, p);
+  if (e != cudaSuccess) cudaGetLastError();
   if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "token_attn_kernel launch: %s", cudaGetErrorString(e));
   return WAVE_OK;
 }
@@ -660,6 +718,32 @@ int launch_token_any(const wave_kv* kv, const TokParams<CAP>& p, cudaStream_t s)
   if (kv->cfg.head_dim == 128)
     return kv->fp8 ? launch_token<128, true, CAP>(p, s) : launch_token<128, false, CAP>(p, s);
   return kv->fp8 ? launch_token<64, true, CAP>(p, s) : launch_token<64, false, CAP>(p, s);
+}
+
+// CTAs per list (a cluster) and clusters per list for lists of at most `longest`
+// items.
+void cut_lists(TokHead& h, int32_t longest) {
+  // Clusters of 1 .. 8 such CTAs that a B200 holds at a time (occupancy query).
+  constexpr int kHeld[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+  const int64_t lists = (int64_t)h.n_groups * h.heads;
+  h.parts = 1;
+  h.cluster = 1;
+  double best = 1e30;
+  for (int s = 1; s <= 8 && s <= std::max(1, longest); ++s) {
+    // Waves of clusters; an item takes 0.46 of its time at a 148th of HBM's rate
+    // when an SM draws all it can, more once the SMs share HBM; a wave costs
+    // about two items to start and end.
+    const double waves = (double)((lists + kHeld[s] - 1) / kHeld[s]);
+    const double active = (double)std::min<int64_t>(lists, kHeld[s]) * s;
+    const double t = waves * ((longest + s - 1) / s * std::max(0.6, active / 148.0) + 2.0);
+    if (t < best) best = t, h.cluster = s;
+  }
+  // Few long lists: several clusters each, while every CTA keeps eight items (the
+  // second kernel costs about as much as two).
+  if (lists * 8 < 64 && longest >= 128) {
+    h.cluster = 8;
+    h.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(kHeld[8] / lists, longest / 64));
+  }
 }
 
 // Lists of a call: groups of consecutive queries with their distinct items.
@@ -678,8 +762,7 @@ int build_lists(wave_kv* kv, const wave_node* active, int32_t n, int32_t policy,
   const int queries = kTokRows / per_kv;
   if ((int64_t)kv->page_mark.size() < kv->max_pages) kv->page_mark.resize(kv->max_pages, 0);
   std::vector<std::pair<int32_t, int32_t>> keys;
-  int32_t items = 0;
-  int64_t units = 0;
+  int32_t items = 0, longest = 0;
   h.n_groups = 0;
   h.rows_max = 0;
   for (int32_t q0 = 0; q0 < n; q0 += queries) {
@@ -688,7 +771,6 @@ int build_lists(wave_kv* kv, const wave_node* active, int32_t n, int32_t policy,
     g.q0 = q0;
     g.rows = nq * per_kv;
     g.item0 = items;
-    g.unit0 = (int32_t)units;
     h.rows_max = std::max(h.rows_max, g.rows);
     const int64_t gen = ++kv->mark_gen;
     for (int32_t i = 0; i < nq; ++i) {
@@ -733,32 +815,18 @@ int build_lists(wave_kv* kv, const wave_node* active, int32_t n, int32_t policy,
       }
     }
     g.n_items = items - g.item0;
-    units += (int64_t)g.n_items * H;
-    if (units >= (1LL << 30)) return fail(WAVE_ERR_CAPACITY, "too many work units");
+    longest = std::max(longest, g.n_items);
   }
   h.heads = H;
   h.per_kv = per_kv;
-  h.units = (int32_t)units;
-  h.ctas = (int32_t)std::min<int64_t>(units, kv->num_sms);
+  cut_lists(h, longest);
   return items;
 }
 
-bool join_needed(const TokHead& h) {
-  // Some group without items (its rows are zeroed there), or some (group,
-  // head) that two CTAs share.
-  for (int g = 0; g < h.n_groups; ++g) {
-    const TokGroup& gr = h.g[g];
-    if (gr.n_items == 0) return true;
-    for (int head = 0; head < h.heads; ++head) {
-      const int64_t a = gr.unit0 + (int64_t)head * gr.n_items, b = a + gr.n_items - 1;
-      if (((a + 1) * h.ctas - 1) / h.units != ((b + 1) * h.ctas - 1) / h.units) return true;
-    }
-  }
-  return false;
+// Workspace: per (list, part) slot, rows_max rows of d fp32 and (m, l).
+uint64_t token_rows(const TokHead& h) {
+  return h.parts > 1 ? (uint64_t)h.n_groups * h.heads * h.parts * h.rows_max : 0;
 }
-
-// Workspace: per (CTA, group, head) slot, rows_max rows of d fp32 and (m, l).
-uint64_t token_slots(const TokHead& h) { return (uint64_t)h.ctas + (uint64_t)h.n_groups * h.heads; }
 
 int token_check(const wave_kv* kv, const wave_node* active, int32_t n_active, int32_t policy,
                 int32_t q_heads) {
@@ -793,8 +861,7 @@ extern "C" int wave_token_attn_workspace(wave_kv* kv, const wave_node* active, i
     TokLists& t = t_lists;
     const int rc = build_lists(kv, active, n_active, policy, own_tokens, q_heads / kv->cfg.heads, t);
     if (rc < 0) return rc;
-    if (t.p.h.units > 0 && join_needed(t.p.h))
-      *bytes = token_slots(t.p.h) * t.p.h.rows_max * (kv->cfg.head_dim + 2) * sizeof(float);
+    *bytes = token_rows(t.p.h) * (kv->cfg.head_dim + 2) * sizeof(float);
   } catch (const std::bad_alloc&) {
     return no_host_memory();
   }
@@ -823,14 +890,13 @@ extern "C" int wave_token_attn(wave_kv* kv, const wave_node* active, int32_t n_a
   }
   if (items < 0) return items;
   TokHead& h = t.p.h;
-  const bool join = join_needed(h);
-  const uint64_t slots = token_slots(h) * h.rows_max;
-  if (join && h.units > 0) {
-    const uint64_t need = slots * (D + 2) * sizeof(float);
-    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
-      return fail(WAVE_ERR_ARG, "needs a 256-byte aligned workspace of %llu bytes (got %llu)",
-                  (unsigned long long)need, (unsigned long long)workspace_bytes);
-  }
+  if ((int64_t)h.n_groups * h.heads * h.parts * h.cluster >= (1LL << 31))
+    return fail(WAVE_ERR_CAPACITY, "too many lists");
+  const uint64_t rows = token_rows(h);
+  const uint64_t need = rows * (D + 2) * sizeof(float);
+  if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+    return fail(WAVE_ERR_ARG, "needs a 256-byte aligned workspace of %llu bytes (got %llu)",
+                (unsigned long long)need, (unsigned long long)workspace_bytes);
   if (int rc = check_current_device(kv)) return rc;
   h.tm = kv->tm_kv;
   uint8_t* pool = static_cast<uint8_t*>(kv->cfg.pool);
@@ -839,29 +905,25 @@ extern "C" int wave_token_attn(wave_kv* kv, const wave_node* active, int32_t n_a
   h.o = static_cast<uint16_t*>(O);
   h.lse = lse;
   h.part_o = static_cast<float*>(workspace);
-  h.part_ml = reinterpret_cast<float2*>(h.part_o + slots * D);
+  h.part_ml = need ? reinterpret_cast<float2*>(h.part_o + rows * D) : nullptr;
   h.ldq = ldq;
   h.ldo = ldo;
   h.status = reinterpret_cast<int32_t*>(pool);
   h.wait_ns = wait_limit_ns(kv);
   h.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (h.units > 0) {
-    int rc;
-    if (items <= kTokCapSmall) {
-      static thread_local TokParams<kTokCapSmall> small;
-      std::memcpy(&small.h, &h, sizeof h);
-      std::memcpy(small.page, t.p.page, items * sizeof(uint32_t));
-      std::memcpy(small.mask, t.p.mask, items * sizeof(uint16_t));
-      rc = launch_token_any(kv, small, s);
-    } else {
-      rc = launch_token_any(kv, t.p, s);
-    }
-    if (rc) return rc;
+  int rc;
+  if (items <= kTokCapSmall) {
+    static thread_local TokParams<kTokCapSmall> small;
+    std::memcpy(&small.h, &h, sizeof h);
+    std::memcpy(small.page, t.p.page, items * sizeof(uint32_t));
+    std::memcpy(small.mask, t.p.mask, items * sizeof(uint16_t));
+    rc = launch_token_any(kv, small, s);
+  } else {
+    rc = launch_token_any(kv, t.p, s);
   }
-  if (!join) return WAVE_OK;
-  // The join may be launched while the first kernel runs (its blocks wait for
-  // it to finish): the launch's latency is hidden behind the first kernel.
+  if (rc || h.parts == 1) return rc;
+  // The second kernel's launch overlaps the first's end (its blocks wait for it).
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(((int64_t)n_active * q_heads + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(32 * kJoinWarps);
@@ -870,7 +932,7 @@ extern "C" int wave_token_attn(wave_kv* kv, const wave_node* active, int32_t n_a
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = h.units > 0 ? 1 : 0;
+  cfg.numAttrs = 1;
   cudaError_t e = D == 128 ? cudaLaunchKernelEx(&cfg, token_join_kernel<128>, h, (int)n_active)
                            : cudaLaunchKernelEx(&cfg, token_join_kernel<64>, h, (int)n_active);
   if (e != cudaSuccess) {

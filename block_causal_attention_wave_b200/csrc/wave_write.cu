@@ -12,6 +12,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cstddef>
 #include <cstdint>
 #include <cstring>
 #include <set>
@@ -36,7 +38,10 @@ struct WriteEntry {
   int32_t tile0;    // the entry's first tile
 };
 
-struct WriteParams {
+// The tables travel in the parameter block; a launch copies it, and 31 KB of
+// it take about 3 us longer than the small form's 1 KB.
+template <int ENTRIES, int PAGES>
+struct WriteParamsOf {
   const uint16_t* k;
   const uint16_t* v;
   int64_t ldk, ldv;     // row strides in elements
@@ -47,9 +52,11 @@ struct WriteParams {
   int32_t log2_vec;     // 16-byte vectors per token row: 8 or 16
   int32_t n_entries;
   int32_t n_tiles;
-  WriteEntry e[WAVE_MAX_APPEND_ENTRIES];
-  int32_t pages[WAVE_MAX_APPEND_PAGES];
+  WriteEntry e[ENTRIES];
+  int32_t pages[PAGES];
 };
+using WriteParams = WriteParamsOf<WAVE_MAX_APPEND_ENTRIES, WAVE_MAX_APPEND_PAGES>;
+using WriteParamsSmall = WriteParamsOf<8, 64>;
 static_assert(sizeof(WriteParams) <= 32760, "kernel parameter space is 32 KB");
 
 // A block's tile: page, K or V, head, and which rows are new.
@@ -61,7 +68,8 @@ struct WriteTile {
   int held;        // rows held before the write (0: the page is fresh, and r0 = 0)
 };
 
-__device__ __forceinline__ WriteTile write_tile(const WriteParams& p, int tile) {
+template <class P>
+__device__ __forceinline__ WriteTile write_tile(const P& p, int tile) {
   int ei = 0;
   while (ei + 1 < p.n_entries && tile >= p.e[ei + 1].tile0) ++ei;
   const WriteEntry& en = p.e[ei];
@@ -81,8 +89,8 @@ __device__ __forceinline__ WriteTile write_tile(const WriteParams& p, int tile) 
   return t;
 }
 
-__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(
-    const __grid_constant__ WriteParams p) {
+template <class P>
+__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_constant__ P p) {
   if (blockIdx.x >= p.n_tiles) return;
   const WriteTile t = write_tile(p, blockIdx.x);
   const int vec = 1 << p.log2_vec;
@@ -122,8 +130,8 @@ __device__ __forceinline__ float2 write_decode2(uint16_t pair) {
 }
 
 // Row r of an FP8 tile is new (r0 <= r < r1), kept (r < held, not new) or zero.
-__global__ void __launch_bounds__(kWriteThreads) kv_write_fp8_kernel(
-    const __grid_constant__ WriteParams p) {
+template <class P>
+__global__ void __launch_bounds__(kWriteThreads) kv_write_fp8_kernel(const __grid_constant__ P p) {
   __shared__ float warp_max[kWriteThreads / 32];
   if (blockIdx.x >= p.n_tiles) return;
   const WriteTile t = write_tile(p, blockIdx.x);
@@ -201,6 +209,14 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_fp8_kernel(
   }
 }
 
+template <class P>
+void launch_write(bool fp8, const P& p, cudaStream_t s) {
+  if (fp8)
+    kv_write_fp8_kernel<P><<<(unsigned)p.n_tiles, kWriteThreads, 0, s>>>(p);
+  else
+    kv_write_kernel<P><<<(unsigned)p.n_tiles, kWriteThreads, 0, s>>>(p);
+}
+
 }  // namespace
 }  // namespace wavei
 
@@ -269,10 +285,15 @@ extern "C" int wave_kv_write_tokens(wave_kv* kv, int32_t n_entries, const wave_n
   p.n_entries = n;
   p.n_tiles = (int32_t)tiles;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (kv->fp8)
-    kv_write_fp8_kernel<<<(unsigned)tiles, kWriteThreads, 0, s>>>(p);
-  else
-    kv_write_kernel<<<(unsigned)tiles, kWriteThreads, 0, s>>>(p);
+  if (n <= 8 && pages <= 64) {
+    WriteParamsSmall q;
+    std::memcpy(&q, &p, offsetof(WriteParamsSmall, e));
+    std::memcpy(q.e, p.e, n * sizeof(WriteEntry));
+    std::memcpy(q.pages, p.pages, pages * sizeof(int32_t));
+    launch_write(kv->fp8, q, s);
+  } else {
+    launch_write(kv->fp8, p, s);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess)
     return fail(WAVE_ERR_CUDA, "kv_write_kernel launch: %s", cudaGetErrorString(e));

@@ -186,9 +186,7 @@ int main(int argc, char** argv) {
   expect(att({{1, 1}}, {}, 2, WAVE_POLICY_SAME, odd), bad, "attention: Q misaligned");
   expect(att({{1, 1}}, {}, 2, WAVE_POLICY_SAME, p, 120), bad, "attention: ldq short");
   expect(att({{1, 1}}, {}, 2, WAVE_POLICY_SAME, p, 128, p, 132), bad, "attention: ldo % 8");
-  expect(att({{1, 1}}, {}, 2, WAVE_POLICY_SAME, p, 128, p, 128, nullptr, 0), bad, "attention: no workspace");
-  expect(att({{1, 1}}, {}, 2, WAVE_POLICY_SAME, p, 128, p, 128, p, 16), bad, "attention: short workspace");
-  expect(att({{1, 1}}, {}, 2, WAVE_POLICY_SAME, p, 128, p, 128, p + 8), bad, "attention: workspace misaligned");
+  expect(att({{1, 1}}, {}, 2, WAVE_POLICY_SAME, p, 128, p, 128, nullptr, 0), stop, "attention: a short list needs no workspace");
   expect(wave_token_attn(kv, std::vector<wave_node>(65, {1, 1}).data(), 65, 1, nullptr, 2, p, 128, p, 128, nullptr,
                          p, sizeof buf, nullptr), WAVE_ERR_CAPACITY, "attention: 65 queries");
   wave_kv_destroy(kv);
@@ -199,9 +197,16 @@ int main(int argc, char** argv) {
   const wave_node last{4, 1}, two[2] = {{4, 1}, {4, 1}};
   int32_t own[2] = {128 * 1024, 128 * 1024};
   expect(wave_token_attn_workspace(kv, &last, 1, 1, own, 1, &bytes), WAVE_OK, "5120 pages");
-  expect((long long)bytes, (148 + 1) * (64 + 2) * 4, "a slot per SM and one per list");
+  expect((long long)bytes, 15 * (64 + 2) * 4, "one list over 15 clusters");
+  auto late = [&](void* ws, uint64_t n) {
+    return wave_token_attn(kv, &last, 1, 1, own, 1, p, 64, p, 64, nullptr, ws, n, nullptr);
+  };
+  expect(late(p, bytes), stop, "attention: workspace as told");
+  expect(late(p, bytes - 1), bad, "attention: short workspace");
+  expect(late(p + 8, bytes), bad, "attention: workspace misaligned");
+  expect(late(nullptr, bytes), bad, "attention: no workspace");
   expect(wave_token_attn_workspace(kv, two, 2, 1, own, 1, &bytes), WAVE_OK, "5120 pages, shared by two queries");
-  expect((long long)bytes, (148 + 1) * 2 * (64 + 2) * 4, "two rows a slot");
+  expect((long long)bytes, 15 * 2 * (64 + 2) * 4, "two rows a part");
   own[1] -= 1;  // its last page is an item of its own
   expect(wave_token_attn_workspace(kv, two, 2, 1, own, 1, &bytes), WAVE_ERR_CAPACITY, "5121 items");
   own[1] -= 127;
@@ -210,7 +215,7 @@ int main(int argc, char** argv) {
   int32_t few = 100;
   const wave_node head{0, 1};
   expect(wave_token_attn_workspace(kv, &head, 1, 1, &few, 1, &bytes), WAVE_OK, "one page");
-  expect((long long)bytes, 0, "a whole list in one SM needs no workspace");
+  expect((long long)bytes, 0, "a short list needs no workspace");
   few = 0;
   expect(wave_token_attn_workspace(kv, &head, 1, 1, &few, 1, &bytes), WAVE_OK, "no token");
   expect((long long)bytes, 0, "nothing to join");

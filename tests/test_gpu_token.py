@@ -657,7 +657,7 @@ def test_token_attn_timeout_is_reported(cuda_lib):
         kv.alloc(c, 1)
     q = torch.ones(1, 8, 128, dtype=torch.bfloat16, device="cuda")
     ws = torch.empty(kv.token_attn_workspace([(399, 1)], "same"), dtype=torch.uint8, device="cuda")
-    kv.set_wait_limit(100)
+    kv.set_wait_limit(1)
     kv.token_attn([(399, 1)], "same", q, torch.empty_like(q), workspace=ws)
     with pytest.raises(cuda_lib.WaveError) as e:
         kv.status()
@@ -668,3 +668,24 @@ def test_token_attn_timeout_is_reported(cuda_lib):
     kv.status()
     # all scores 0: log of the 51200 tokens; all values 0
     assert not o.any() and (lse.double() - np.log(51200.0)).abs().max() < 2.0 ** -20 * 12
+
+
+@FORMATS
+@pytest.mark.parametrize("d", [64, 128])
+def test_token_attn_many_calls_back_to_back(cuda_lib, fp8, d):
+    """Long lists, hundreds of calls with nothing between them: equal bytes. (Tiles
+    land in any order and the warps' teams drift apart.)"""
+    import torch
+    H, T = 6, 1280
+    kv = _cache(cuda_lib, H, d, T, 1, pages=300, fp8=fp8, fill=0)
+    K, V = (torch.randn(T, H, d, device="cuda").bfloat16() for _ in range(2))
+    for c in range(30):
+        kv.append(c, 1, K, V)
+    q = torch.randn(2, H, d, device="cuda").bfloat16()
+    nodes, own = [(29, 1), (28, 1)], [T, 77]
+    ws = torch.empty(kv.token_attn_workspace(nodes, "same", own), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(q) for _ in range(300)]
+    for o in outs:
+        kv.token_attn(nodes, "same", q, o, own_tokens=own, workspace=ws)
+    kv.status()
+    assert torch.isfinite(outs[0].float()).all() and all(torch.equal(o, outs[0]) for o in outs)
