@@ -1,0 +1,87 @@
+// wave_linear_bias: its checks, and which kernel takes a call.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "wave_dense.cuh"
+#include "wave_internal.h"
+
+namespace wavei {
+namespace {
+
+// Up to 16 rows: token_rows_kernel (wave_few.cu). Blocks of 16 features where they
+// still give every SM two (one token, us: 1536 -> 8960 7.8, 8-feature blocks 8.4;
+// 1536 -> 1536 5.0 and 3.9); 16 warps to a block where K is long and the blocks
+// few (8960 -> 1536: 10.0, with 8 warps 12.5; 1536 -> 1536: 4.4 and 3.9).
+int launch_tokens(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
+  if (a.N >= 2 * 16 * kv->num_sms) return token_rows_launch(a, 2, 8, s);
+  return token_rows_launch(a, 1, a.K >= 4096 && a.M <= 8 ? 16 : 8, s);
+}
+
+// More rows: the cheapest form by its cost in us: a start and end, and what a
+// 64-wide slice of K takes, which is the issuing thread's time per slice more
+// than the tile's size (measured; a B200 holds kHeld[c] clusters of c CTAs at a
+// time). 984 x 8960 x 1536: pairs with K in two 35.5, in one 53.5, 128-column
+// tiles 49.6; 256 x 1536 x 1536: 64-column tiles with K in two 10.8, pairs 15.3;
+// 512 x 1536 x 4608: 128-column tiles 15.6, pairs 18.6, 64-column tiles 24.8;
+// 2000 x 1536 x 8960: pairs 52.5, 128-column tiles 110.
+int launch_rows(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
+  constexpr int kHeld[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+  struct Form {
+    int rows, cols, ctas, most;  // tile, CTAs that share one, most parts of K
+    double start, slice;
+  };
+  constexpr Form kForms[3] = {{128, 64, 1, 8, 6.5, 0.28}, {128, 128, 1, 8, 8.0, 0.30}, {256, 256, 2, 4, 10.0, 0.32}};
+  const int64_t slices = (a.K + 63) / 64;
+  double best = 1e30;
+  int form = 2, parts = 1;
+  for (int f = 0; f < 3; ++f)
+    for (int n = 1; n <= kForms[f].most && n <= slices; ++n) {
+      const Form& x = kForms[f];
+      const int64_t tiles = ((int64_t)a.M + x.rows - 1) / x.rows * ((a.N + x.cols - 1) / x.cols);
+      const int64_t held = std::max(1, kHeld[x.ctas * n] * kv->num_sms / 148);
+      const double waves = (double)((tiles + held - 1) / held);
+      // Pairs that do not share K are persistent: their tiles follow without a gap.
+      const bool persistent = f == 2 && n == 1;
+      const double t = (persistent ? 1.0 : waves) * (x.start + (n > 1 ? 1.0 : 0.0)) +
+                       waves * (double)((slices + n - 1) / n) * x.slice;
+      if (t < best) best = t, form = f, parts = n;
+    }
+  if (form == 2) return pair_rows_launch(kv, a, parts, s);
+  return split_rows_launch(kv, a, kForms[form].cols, parts, s);
+}
+
+}  // namespace
+}  // namespace wavei
+
+using namespace wavei;
+
+extern "C" int wave_linear_bias(wave_kv* kv, const void* A, int64_t lda, int32_t M, int32_t K,
+                                const void* W, int32_t N, const void* bias, const void* R,
+                                int64_t ldr, int32_t act, void* Y, int64_t ldy, void* stream) {
+  clear_error();
+  if (!kv) return fail(WAVE_ERR_ARG, "NULL handle");
+  if (!kv->on_device) return fail(WAVE_ERR_ARG, "host-only handle (pool == NULL) cannot launch");
+  if (M < 0 || K < 8 || K % 8 != 0 || K > (1 << 16) || N < 8 || N % 8 != 0 || N > (1 << 16))
+    return fail(WAVE_ERR_ARG, "need M >= 0, K and N positive multiples of 8 (at most 65536); got "
+                "M %d, K %d, N %d", M, K, N);
+  if ((int64_t)M * N >= (1LL << 40)) return fail(WAVE_ERR_ARG, "M x N too large");
+  if (act < WAVE_ACT_NONE || act > WAVE_ACT_SILU) return fail(WAVE_ERR_ARG, "unknown activation %d", act);
+  const int64_t most = 1LL << 38;  // the tensor map's stride is below 2^40 bytes
+  if (lda < K || lda % 8 || lda >= most || ldy < N || ldy % 8 || ldy >= most ||
+      (R && (ldr < N || ldr % 8 || ldr >= most)))
+    return fail(WAVE_ERR_ARG, "row strides must be multiples of 8 and cover the row; got lda %lld, "
+                "ldr %lld, ldy %lld", (long long)lda, (long long)ldr, (long long)ldy);
+  if (R && R == Y && ldr != ldy) return fail(WAVE_ERR_ARG, "Y = R needs ldy = ldr");
+  if (M == 0) return WAVE_OK;
+  if (!A || !W || !Y || !aligned16(A) || !aligned16(W) || !aligned16(Y) || (R && !aligned16(R)) ||
+      (bias && !aligned16(bias)))
+    return fail(WAVE_ERR_ARG, "A, W, Y (and bias, R) must be non-NULL and 16-byte aligned");
+  if (int rc = check_current_device(kv)) return rc;
+  if (((int64_t)M + 127) / 128 * ((N + 63) / 64) >= (1LL << 27)) return fail(WAVE_ERR_ARG, "M x N too large");
+  const DenseArgs a{A, lda, M, K, W, N, static_cast<const uint16_t*>(bias), static_cast<const uint16_t*>(R),
+                    ldr, act, static_cast<uint16_t*>(Y), ldy};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return M <= 16 ? launch_tokens(kv, a, s) : launch_rows(kv, a, s);
+}

@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
 #include "wave.h"
 
 namespace wavei {
@@ -24,6 +25,102 @@ __device__ __forceinline__ float activate(float x) {
   if constexpr (ACT == WAVE_ACT_GELU_ERF) return 0.5f * x * (1.f + erff(0.7071067811865476f * x));
   if constexpr (ACT == WAVE_ACT_SILU) return __fdividef(x, 1.f + __expf(-x));
   return x;
+}
+
+// Bias and residual of eight columns of a row, fetched ahead of their use (a trip
+// to L2 is as long as a tile's 32 columns take): P has bias, resid, ldr, y, ldy.
+struct Eight {
+  uint4 b, r;
+};
+template <class P>
+__device__ __forceinline__ Eight fetch8(const P& p, int64_t m, int col, bool in) {
+  Eight e{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (in && p.bias) e.b = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
+  if (in && p.resid) e.r = *reinterpret_cast<const uint4*>(p.resid + m * p.ldr + col);
+  return e;
+}
+// Element i of eight bf16.
+__device__ __forceinline__ float bf16_at(const uint4& v, int i) {
+  const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+  return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+}
+// act(f + bias) + R, as eight bf16.
+template <int ACT>
+__device__ __forceinline__ uint4 finish8(const float (&f)[8], const Eight& e) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(f[i] + bf16_at(e.b, i)) + bf16_at(e.r, i);
+  return make_uint4(wptx::pack_bf16x2(v[0], v[1]), wptx::pack_bf16x2(v[2], v[3]),
+                    wptx::pack_bf16x2(v[4], v[5]), wptx::pack_bf16x2(v[6], v[7]));
+}
+
+// Sum partial tiles [source][row][stride] (fp32, shared memory) of `rows` rows x
+// `cols` columns in source order, finish and store them; row 0 is row m0 of Y,
+// column 0 its column col0. `ready` is called once, after the first bias and
+// residual loads are under way and before any partial is read.
+template <int ACT, int THREADS, class P, class F>
+__device__ __forceinline__ void sum_tiles(const P& p, const float* part, int sources, int per, int stride, int rows,
+                                          int cols, int64_t m0, int col0, F ready) {
+  constexpr int kBatch = 4;
+  const int vec = cols >> 3, total = max(rows, 0) * vec;
+  Eight e[kBatch];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * THREADS, r = i / vec;
+      e[k] = fetch8(p, m0 + r, col0 + (i - r * vec) * 8, i < total);
+    }
+  };
+  fetch(threadIdx.x);
+  ready();
+  for (int i0 = threadIdx.x; i0 < total; i0 += kBatch * THREADS) {
+    if (i0 != (int)threadIdx.x) fetch(i0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * THREADS, r = i / vec, c = (i - r * vec) * 8;
+      if (i >= total) break;
+      float f[8] = {};
+      for (int s = 0; s < sources; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(part + (s * per + r) * stride + c);
+        const float4 lo = src[0], hi = src[1];
+        f[0] += lo.x; f[1] += lo.y; f[2] += lo.z; f[3] += lo.w;
+        f[4] += hi.x; f[5] += hi.y; f[6] += hi.z; f[7] += hi.w;
+      }
+      *reinterpret_cast<uint4*>(p.y + (m0 + r) * p.ldy + col0 + c) = finish8<ACT>(f, e[k]);
+    }
+  }
+}
+
+// Columns c0 .. c1 - 1 (of p.N) of one row from TMEM (column 0 of the tile at
+// `tmem`), finished and stored, 32 at a time with the next 32 columns' bias and
+// residual on their way. All 32 lanes call it; `in`: the lane's row exists.
+// `ready`: called after the first loads, before TMEM is read.
+template <int ACT, class P, class F>
+__device__ __forceinline__ void finish_row(const P& p, uint32_t tmem, int64_t m, int col0, int c0, int c1, bool in,
+                                           F ready) {
+  Eight e[4], n[4];
+  auto fetch = [&](Eight (&x)[4], int c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = fetch8(p, m, col0 + c + 8 * j, in && c + 8 * j < c1 && col0 + c + 8 * j < p.N);
+  };
+  fetch(e, c0);
+  if (!ready()) return;
+#pragma unroll 1
+  for (int c = c0; c < c1 && col0 + c < p.N; c += 32) {
+    fetch(n, c + 32);
+    uint32_t v[32];
+    wptx::tmem_ld32_wait(tmem + c, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * j + i]);
+      const uint4 out = finish8<ACT>(f, e[j]);
+      if (in && col0 + c + 8 * j < p.N) *reinterpret_cast<uint4*>(p.y + m * p.ldy + col0 + c + 8 * j) = out;
+      e[j] = n[j];
+    }
+    __syncwarp();  // reconverge before the next tcgen05.ld
+  }
 }
 
 // A checked call of wave_linear_bias.
@@ -46,10 +143,14 @@ struct DenseArgs {
 int encode_kmajor(CUtensorMap* map, const void* base, int64_t rows, int64_t k, uint32_t box_rows,
                   const char* what, int64_t ld = 0);
 
-// wave_few.cu. At most 16 rows, blocks of 8 ft features (ft = 1 or 2) and 8 or 16 warps.
+// wave_few.cu. At most 16 rows, blocks of 8 ft features (ft = 1 or 2) and 8 warps,
+// or (ft = 1, at most 8 rows) 16.
 int token_rows_launch(const DenseArgs& a, int ft, int warps, cudaStream_t s);
-// wave_few.cu. Tiles of 128 rows x nf features (64, 128 or 256), K cut over clusters
-// of `splits` CTAs (1 .. 8, at most the 64-wide slices of K).
+// wave_few.cu. Tiles of 128 rows x nf features (64 or 128), K cut over clusters of
+// `splits` CTAs (1 .. 8, at most the 64-wide slices of K).
 int split_rows_launch(const struct ::wave_kv* kv, const DenseArgs& a, int nf, int splits, cudaStream_t s);
+// wave_pair.cu. Tiles of 256 x 256 on pairs of SMs; splits > 1 (2 .. 4, at most the
+// 64-wide slices of K): K cut over the pairs of a cluster.
+int pair_rows_launch(const struct ::wave_kv* kv, const DenseArgs& a, int splits, cudaStream_t s);
 
 }  // namespace wavei

@@ -197,28 +197,28 @@ struct SplitParams {
   int64_t ldr, ldy;
 };
 
+// The four K = 16 steps of a 64-wide slice in one block: low descriptor words
+// a, b and 32 bytes on for each step, common high word.
+__device__ __forceinline__ void mma_slice(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y;\n\t.reg .b32 l, m;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, %5, %5;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t"
+      "add.u32 l, %1, 2;\n\tadd.u32 m, %2, 2;\n\tmov.b64 x, {l, %3};\n\tmov.b64 y, {m, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+      "add.u32 l, %1, 4;\n\tadd.u32 m, %2, 4;\n\tmov.b64 x, {l, %3};\n\tmov.b64 y, {m, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+      "add.u32 l, %1, 6;\n\tadd.u32 m, %2, 6;\n\tmov.b64 x, {l, %3};\n\tmov.b64 y, {m, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc),
+      "r"(accumulate)
+      : "memory");
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-}
-// act(f + bias) + R of eight columns of one row, stored.
-template <int ACT>
-__device__ __forceinline__ void finish8(const SplitParams& p, int64_t m, int col, float (&f)[8]) {
-  float b[8] = {}, r[8] = {};
-  if (p.bias) load8(p.bias + col, b);
-  if (p.resid) load8(p.resid + m * p.ldr + col, r);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = activate<ACT>(f[e] + b[e]) + r[e];
-  *reinterpret_cast<uint4*>(p.y + m * p.ldy + col) =
-      make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                 pack_bf16x2(f[6], f[7]));
-}
-
 template <int NF, int ACT>
 __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __grid_constant__ SplitParams p) {
   using C = SplitCfg<NF>;
@@ -266,32 +266,34 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
       // Rows past box_rows are left as they are: they only reach unused rows.
       const uint32_t bytes = NF * 128 + p.box_rows * 128;
       int n = 0;
+      int s = 0;
+      uint32_t ph = 1;
       for (int k = k0; k < k1; ++k, ++n) {
-        const int s = n % S;
-        if (n >= S && !wait_bar(bar(C::kEmpty + s), (n / S - 1) & 1, ctl, 0x501)) break;
+        if (n >= S && !wait_bar_fast(bar(C::kEmpty + s), ph, ctl, 0x501)) break;
         mbar_arrive_expect_tx(bar(C::kFull + s), bytes);
         tma_load_2d(sb + s * C::kStage + C::kATile, &p.tm_w, k * 64, ft * NF, bar(C::kFull + s));
         tma_load_2d(sb + s * C::kStage, &p.tm_a, k * 64, mt * 128, bar(C::kFull + s));
+        if (++s == S) s = 0, ph ^= 1;
       }
       // Copies still in flight land before the ring is reused or the CTA exits.
       for (int k = n > S ? n - S : 0; k < n; ++k) drain_wait(bar(C::kFull + k % S), (k / S) & 1);
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      const uint64_t desc = desc_k(sb);
+      const uint32_t hi = (uint32_t)(desc >> 32), lo0 = (uint32_t)desc;
       bool ok = true;
+      int s = 0;
+      uint32_t ph = 0;
       for (int n = 0; n < k1 - k0; ++n) {
-        const int s = n % S;
-        if (!wait_bar(bar(C::kFull + s), (n / S) & 1, ctl, 0x502)) {
+        if (!wait_bar_fast(bar(C::kFull + s), ph, ctl, 0x502)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint32_t a = sb + s * C::kStage;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss(tmem, desc_k(a + kk * 32), desc_k(a + C::kATile + kk * 32), C::kIdesc,
-                 (n | kk) != 0 ? 1u : 0u);
+        const uint32_t lo = lo0 + (uint32_t)s * (C::kStage >> 4);
+        mma_slice(tmem, lo, lo + (C::kATile >> 4), hi, C::kIdesc, n != 0);
         tc_commit(bar(C::kEmpty + s));
+        if (++s == S) s = 0, ph ^= 1;
       }
       if (ok) tc_commit(bar(C::kAccFull));
       // Every MMA issued above completes before TMEM is released.
@@ -299,31 +301,22 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
       drain_wait(bar(C::kDrain), 0);
     }
   } else {
-    // Thread: row of the tile (TMEM lane; warp w may read lanes 32 (w % 4) ..).
-    __all_sync(0xffffffffu, wait_bar(bar(C::kAccFull), 0, ctl, 0x503));
-    tc_fence_after();
+    if (p.splits > 1) {
+      __all_sync(0xffffffffu, wait_bar(bar(C::kAccFull), 0, ctl, 0x503));
+      tc_fence_after();
+    }
   }
   __syncwarp();
+  // Thread of warps 2..5: row of the tile (TMEM lane; warp w may read lanes 32 (w % 4) ..).
   const int row = (warp & 3) * 32 + lane;
   const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
   if (p.splits == 1) {
-    if (warp >= 2) {
-#pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
-        uint32_t v[32];
-        tmem_ld32_wait(trow + c, v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (row < rows && c + 8 * j < cols) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * j + e]);
-            finish8<ACT>(p, (int64_t)mt * 128 + row, ft * NF + c + 8 * j, f);
-          }
-        }
-        __syncwarp();  // reconverge before the next tcgen05.ld
-      }
-    }
+    if (warp >= 2)
+      finish_row<ACT>(p, trow, (int64_t)mt * 128 + row, ft * NF, 0, NF, row < rows, [&] {
+        const bool ok = __all_sync(0xffffffffu, wait_bar(bar(C::kAccFull), 0, ctl, 0x503));
+        tc_fence_after();
+        return ok;
+      });
   } else {
     // Sum the cluster's partial tiles: the CTA of rank o gets rows o * per ..
     // of every CTA's tile, as [source rank][row][kPartRow], in its ring.
@@ -349,22 +342,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
       }
     }
     __syncwarp();
-    cluster_sync();
-    const float* part = reinterpret_cast<const float*>(smem);
-    const int mine = min(per, rows - rank * per);  // may be <= 0 for the last ranks
-    const int vec = cols >> 3;
-    for (int i = threadIdx.x; i < mine * vec; i += kSplitThreads) {
-      const int r = i / vec, c = (i - r * vec) * 8;
-      float f[8] = {};
-      for (int s = 0; s < p.splits; ++s) {
-        const float4* src = reinterpret_cast<const float4*>(part + (s * per + r) * C::kPartRow + c);
-        const float4 lo = src[0], hi = src[1];
-        f[0] += lo.x; f[1] += lo.y; f[2] += lo.z; f[3] += lo.w;
-        f[4] += hi.x; f[5] += hi.y; f[6] += hi.z; f[7] += hi.w;
-      }
-      finish8<ACT>(p, (int64_t)mt * 128 + rank * per + r, ft * NF + c, f);
-    }
+    sum_tiles<ACT, kSplitThreads>(p, reinterpret_cast<const float*>(smem), p.splits, per, C::kPartRow,
+                                  min(per, rows - rank * per), cols, (int64_t)mt * 128 + rank * per, ft * NF,
+                                  [] { __syncwarp(); cluster_sync(); });
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -418,13 +400,9 @@ int token_rows_launch(const DenseArgs& a, int ft, int warps, cudaStream_t s) {
   const TokenRowsParams p{static_cast<const uint16_t*>(a.A), static_cast<const uint16_t*>(a.W), a.Y, a.R, a.bias,
                           a.lda, a.ldr, a.ldy, a.M, a.K, a.N};
   const bool r16 = a.M > 8;
-  if (warps == 16) {
-    if (ft == 1) r16 ? launch_token_rows<16, 1, true>(p, a.act, s) : launch_token_rows<16, 1, false>(p, a.act, s);
-    else r16 ? launch_token_rows<16, 2, true>(p, a.act, s) : launch_token_rows<16, 2, false>(p, a.act, s);
-  } else {
-    if (ft == 1) r16 ? launch_token_rows<8, 1, true>(p, a.act, s) : launch_token_rows<8, 1, false>(p, a.act, s);
-    else r16 ? launch_token_rows<8, 2, true>(p, a.act, s) : launch_token_rows<8, 2, false>(p, a.act, s);
-  }
+  if (warps == 16) launch_token_rows<16, 1, false>(p, a.act, s);
+  else if (ft == 1) r16 ? launch_token_rows<8, 1, true>(p, a.act, s) : launch_token_rows<8, 1, false>(p, a.act, s);
+  else r16 ? launch_token_rows<8, 2, true>(p, a.act, s) : launch_token_rows<8, 2, false>(p, a.act, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "token_rows_kernel launch: %s", cudaGetErrorString(e));
   return WAVE_OK;
@@ -448,9 +426,7 @@ int split_rows_launch(const wave_kv* kv, const DenseArgs& a, int nf, int splits,
   p.ldr = a.ldr;
   p.ldy = a.ldy;
   const int tiles = p.n_ftiles * ((a.M + 127) / 128);
-  if (nf == 64) return launch_split_act<64>(p, tiles, a.act, s);
-  if (nf == 128) return launch_split_act<128>(p, tiles, a.act, s);
-  return launch_split_act<256>(p, tiles, a.act, s);
+  return nf == 64 ? launch_split_act<64>(p, tiles, a.act, s) : launch_split_act<128>(p, tiles, a.act, s);
 }
 
 }  // namespace wavei

@@ -40,7 +40,6 @@
 #include <cstring>
 #include <mutex>
 #include <string>
-#include <type_traits>
 #include <vector>
 
 #include "ptx.cuh"
@@ -107,20 +106,6 @@ struct GemmParams {
 };
 static_assert(sizeof(GemmParams) <= 32760, "kernel parameter space is 32 KB");
 
-// The form with bias has parameters of its own: a launch copies its parameter
-// block, and 32 KB of it take about 3 us longer than a few hundred bytes.
-struct LinearParams {
-  CUtensorMap tm_a, tm_b;
-  int32_t* status;
-  uint64_t wait_ns;
-  int32_t k_slices, n_mtiles, n_ntiles, n_tiles;
-  int32_t M, N;
-  uint16_t* y;
-  const uint16_t* resid;   // or null
-  const uint16_t* bias;    // [N] or null
-  int64_t ldr, ldy;        // row strides of R and Y
-};
-
 // sin and cos of a rotary angle: reduced to [-pi, pi] by subtracting the
 // nearest multiple of 2 pi (Cody-Waite: 2 pi split into 6.28125, exact in a
 // few bits, plus the remainder, so k * 6.28125 is exact for the k that occur),
@@ -132,7 +117,6 @@ __device__ __forceinline__ void rope_sincos(float a, float* sn, float* cs) {
   __sincosf(r, sn, cs);
 }
 
-__device__ __forceinline__ int64_t a_row0(const LinearParams&, int mt) { return (int64_t)mt * 128; }
 __device__ __forceinline__ int64_t a_row0(const GemmParams& p, int mt) {
   if (p.mode == MODE_QKV) {
     const int node = mt / p.mt_per_node;
@@ -141,21 +125,8 @@ __device__ __forceinline__ int64_t a_row0(const GemmParams& p, int mt) {
   return (int64_t)mt * 128;
 }
 
-// Element e of eight bf16 in a 16-byte vector.
-__device__ __forceinline__ float bf16_at(const uint4& v, int e) {
-  const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-  return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
-}
-
-// Forms: the round's layers (-1), or a dense layer with bias, row strides and an
-// N that need not fill a tile (N a multiple of 8), one form per activation.
-constexpr int kRoundForm = -1;
-template <int FORM>
-using FormParams = std::conditional_t<FORM == kRoundForm, GemmParams, LinearParams>;
-
-template <int FORM>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    gemm_wide_kernel(const __grid_constant__ FormParams<FORM> p) {
+    gemm_wide_kernel(const __grid_constant__ GemmParams p) {
   using C = GemmCfg;
   constexpr int S = kGemmStages;
   extern __shared__ uint8_t smem_raw[];
@@ -260,39 +231,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const int mt = t / n_n, nt = t - mt * n_n;
-      if constexpr (FORM != kRoundForm) {
-        const int64_t r = (int64_t)mt * 128 + row;
-        const bool in = r < p.M;
-        uint16_t* yr = p.y + r * p.ldy;
-        const uint16_t* rr = p.resid ? p.resid + r * p.ldr : nullptr;
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          const int col0 = nt * 256 + 32 * c;
-          if (col0 >= p.N) break;
-          const int n8 = min(4, (p.N - col0) >> 3);  // 8-column vectors inside N
-          uint4 b4[4], r4[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            b4[j] = r4[j] = make_uint4(0, 0, 0, 0);
-            if (p.bias && j < n8) b4[j] = __ldg(reinterpret_cast<const uint4*>(p.bias + col0) + j);
-            if (rr && in && j < n8) r4[j] = *(reinterpret_cast<const uint4*>(rr + col0) + j);
-          }
-          uint32_t v[32];
-          tmem_ld32_wait(trow + 256 * acc + 32 * c, v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              f[e] = activate<FORM>(__uint_as_float(v[8 * j + e]) + bf16_at(b4[j], e)) + bf16_at(r4[j], e);
-            if (in && j < n8)
-              *(reinterpret_cast<uint4*>(yr + col0) + j) =
-                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-          }
-          __syncwarp();  // rows past M skip the store: reconverge before the next tcgen05.ld
-        }
-      } else if (p.mode == MODE_LINEAR) {
+      if (p.mode == MODE_LINEAR) {
         const int64_t r = (int64_t)mt * 128 + row;
         const bool in = r < p.M;
 #pragma unroll 1
@@ -401,17 +340,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-template <int FORM = kRoundForm>
-int launch_gemm(const FormParams<FORM>& prm, int grid, cudaStream_t stream) {
+int launch_gemm(const GemmParams& prm, int grid, cudaStream_t stream) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_wide_kernel<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    attr_err = cudaFuncSetAttribute(gemm_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     GemmCfg::kSmemBytes);
   });
   if (attr_err != cudaSuccess)
     return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
-  gemm_wide_kernel<FORM><<<grid, kGemmThreads, GemmCfg::kSmemBytes, stream>>>(prm);
+  gemm_wide_kernel<<<grid, kGemmThreads, GemmCfg::kSmemBytes, stream>>>(prm);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "gemm_wide_kernel launch: %s", cudaGetErrorString(e));
   return WAVE_OK;
@@ -486,49 +424,7 @@ int qkv_wide_launch(wave_kv* kv, int32_t n, const wave_node* nodes, int32_t T, c
     prm.node_chunk[i] = nodes[i].chunk;
     std::memcpy(prm.pages + i * mt_per_node, ent.pages.data(), mt_per_node * sizeof(int32_t));
   }
-  return launch_gemm<>(prm, std::min(prm.n_tiles, kv->num_sms), static_cast<cudaStream_t>(stream));
-}
-
-static int wide_bias_launch(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
-  LinearParams prm = {};
-  if (int rc = encode_kmajor(&prm.tm_a, a.A, a.M, a.K, 128, "A", a.lda)) return rc;
-  if (int rc = encode_kmajor(&prm.tm_b, a.W, a.N, a.K, 256, "W")) return rc;
-  prm.status = static_cast<int32_t*>(kv->cfg.pool);
-  prm.wait_ns = wait_limit_ns(kv);
-  prm.k_slices = (a.K + 63) / 64;  // the tensor maps fill K's tail with zeros
-  prm.n_mtiles = (int)(((int64_t)a.M + 127) / 128);
-  prm.n_ntiles = (a.N + 255) / 256;
-  if ((int64_t)prm.n_mtiles * prm.n_ntiles >= (1LL << 30)) return fail(WAVE_ERR_ARG, "M x N too large");
-  prm.n_tiles = prm.n_mtiles * prm.n_ntiles;
-  prm.M = a.M;
-  prm.N = a.N;
-  prm.y = a.Y;
-  prm.resid = a.R;
-  prm.bias = a.bias;
-  prm.ldr = a.ldr;
-  prm.ldy = a.ldy;
-  const int grid = std::min(prm.n_tiles, kv->num_sms);
-  switch (a.act) {
-    case WAVE_ACT_GELU_TANH: return launch_gemm<WAVE_ACT_GELU_TANH>(prm, grid, s);
-    case WAVE_ACT_GELU_ERF: return launch_gemm<WAVE_ACT_GELU_ERF>(prm, grid, s);
-    case WAVE_ACT_SILU: return launch_gemm<WAVE_ACT_SILU>(prm, grid, s);
-    default: return launch_gemm<WAVE_ACT_NONE>(prm, grid, s);
-  }
-}
-
-// Which kernel: see wave_few.cu for the one that is not the wide GEMM.
-static int dense_launch(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
-  const char* force = std::getenv("WAVE_DENSE");  // PROBE
-  if (force) {
-    int nt = 0, sp = 0;
-    sscanf(force, "%d,%d", &nt, &sp);
-    if (nt && nt <= 4) return token_rows_launch(a, nt, sp, s);
-    if (nt) return split_rows_launch(kv, a, nt, std::min(sp, (a.K + 63) / 64), s);
-    return wide_bias_launch(kv, a, s);
-  }
-  if (a.M > 128) return wide_bias_launch(kv, a, s);
-  if (a.M <= 16) return token_rows_launch(a, 2, 8, s);
-  return split_rows_launch(kv, a, 128, std::min(3, (a.K + 63) / 64), s);
+  return launch_gemm(prm, std::min(prm.n_tiles, kv->num_sms), static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace wavei
@@ -617,32 +513,5 @@ extern "C" int wave_linear(wave_kv* kv, const void* A, int32_t M, int32_t K, con
   prm.act = act;
   prm.y = static_cast<uint16_t*>(Y);
   prm.resid = static_cast<const uint16_t*>(R);
-  return launch_gemm<>(prm, std::min(prm.n_tiles, kv->num_sms), static_cast<cudaStream_t>(stream));
-}
-
-extern "C" int wave_linear_bias(wave_kv* kv, const void* A, int64_t lda, int32_t M, int32_t K,
-                                const void* W, int32_t N, const void* bias, const void* R,
-                                int64_t ldr, int32_t act, void* Y, int64_t ldy, void* stream) {
-  clear_error();
-  if (!kv) return fail(WAVE_ERR_ARG, "NULL handle");
-  if (!kv->on_device) return fail(WAVE_ERR_ARG, "host-only handle (pool == NULL) cannot launch");
-  if (M < 0 || K < 8 || K % 8 != 0 || K > (1 << 16) || N < 8 || N % 8 != 0 || N > (1 << 16))
-    return fail(WAVE_ERR_ARG, "need M >= 0, K and N positive multiples of 8 (at most 65536); got "
-                "M %d, K %d, N %d", M, K, N);
-  if ((int64_t)M * N >= (1LL << 40)) return fail(WAVE_ERR_ARG, "M x N too large");
-  if (act < WAVE_ACT_NONE || act > WAVE_ACT_SILU) return fail(WAVE_ERR_ARG, "unknown activation %d", act);
-  const int64_t most = 1LL << 38;  // the tensor map's stride is below 2^40 bytes
-  if (lda < K || lda % 8 || lda >= most || ldy < N || ldy % 8 || ldy >= most ||
-      (R && (ldr < N || ldr % 8 || ldr >= most)))
-    return fail(WAVE_ERR_ARG, "row strides must be multiples of 8 and cover the row; got lda %lld, "
-                "ldr %lld, ldy %lld", (long long)lda, (long long)ldr, (long long)ldy);
-  if (R && R == Y && ldr != ldy) return fail(WAVE_ERR_ARG, "Y = R needs ldy = ldr");
-  if (M == 0) return WAVE_OK;
-  if (!A || !W || !Y || !aligned16(A) || !aligned16(W) || !aligned16(Y) || (R && !aligned16(R)) ||
-      (bias && !aligned16(bias)))
-    return fail(WAVE_ERR_ARG, "A, W, Y (and bias, R) must be non-NULL and 16-byte aligned");
-  if (int rc = check_current_device(kv)) return rc;
-  const DenseArgs a{A, lda, M, K, W, N, static_cast<const uint16_t*>(bias), static_cast<const uint16_t*>(R),
-                    ldr, act, static_cast<uint16_t*>(Y), ldy};
-  return dense_launch(kv, a, static_cast<cudaStream_t>(stream));
+  return launch_gemm(prm, std::min(prm.n_tiles, kv->num_sms), static_cast<cudaStream_t>(stream));
 }

@@ -529,18 +529,28 @@ __global__ void __launch_bounds__(kTokThreads, 1)
       return true;
     };
     int f = 0;   // the team's fills taken
+    // The next unit's table words and scales are fetched a unit ahead: a scale is a
+    // trip to L2, which a unit of its own could not hide.
+    uint32_t next_word = 0, next_mask = 0;
+    float next_sk = 1.f, next_sv = 1.f;
+    auto fetch = [&](int u) {
+      if (u >= u1) return;
+      next_word = pages[u];
+      next_mask = masks[u];
+      if constexpr (FP8) {
+        const int64_t page = next_word & 0x1FFFFFFu;
+        next_sk = __ldg(h.scales + (page * 2) * h.heads + head);
+        next_sv = __ldg(h.scales + (page * 2 + 1) * h.heads + head);
+      }
+    };
+    fetch(u0 + team);
     for (int u = u0 + team; u < u1; u += kTokTeams) {
       const int ks = f % S, kp = (f / S) & 1, vs = (f + 1) % S, vp = ((f + 1) / S) & 1;
       f += 2;
-      const int seen = (int)(pages[u] >> 25) + 1;
-      const uint32_t mask = masks[u];
-      float sk = 1.f, sv = 1.f;
-      if constexpr (FP8) {
-        // Two loads that are in flight while the tile is waited for.
-        const int64_t page = pages[u] & 0x1FFFFFFu;
-        sk = __ldg(h.scales + (page * 2) * h.heads + head);
-        sv = __ldg(h.scales + (page * 2 + 1) * h.heads + head);
-      }
+      const int seen = (int)(next_word >> 25) + 1;
+      const uint32_t mask = next_mask;
+      const float sk = next_sk, sv = next_sv;
+      fetch(u + kTokTeams);
       if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(full(ks), kp, ctl, 0x402));
       if (dead) continue;
       // The common unit, of which every row sees every token, has code of its own:
