@@ -8,6 +8,7 @@ There is no fallback: if the library is missing, ``load()`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -204,17 +205,33 @@ def _policy(policy) -> int:
     return POLICIES[policy] if isinstance(policy, str) else int(policy)
 
 
+@functools.lru_cache(maxsize=None)
+def _node_array(n):
+    return Node * max(1, n)
+
+
 def _nodes(active):
-    arr = (Node * max(1, len(active)))()
-    for i, (c, l) in enumerate(active):
-        arr[i].chunk, arr[i].level = int(c), int(l)
+    arr = _node_array(len(active))()
+    for a, (c, l) in zip(arr, active):
+        a.chunk, a.level = int(c), int(l)
     return arr
+
+
+@functools.lru_cache(maxsize=None)
+def _int_array(n):
+    return ctypes.c_int32 * max(1, n)
 
 
 def _ints(values, n, what):
     if len(values) != n:
         raise ValueError(f"{what}: {n} values wanted, got {len(values)}")
-    return (ctypes.c_int32 * max(1, n))(*values)
+    return _int_array(n)(*values)
+
+
+@functools.lru_cache(maxsize=256)
+def _rotary_spec(pairs, base, layout, ladder, inverse):
+    return ctypes.pointer(RotarySpec(pairs, base, ROTARY_LAYOUTS[layout], ROTARY_LADDERS[ladder],
+                                     inverse))
 
 
 def _stream_handle(stream):
@@ -395,18 +412,21 @@ class KVCache:
         ``width`` contiguous elements: 2-D [rows][width], or [rows][heads][d]
         with contiguous heads. A kernel would read a host tensor's address, or
         past a short one, as readily as a good one, so both are refused here."""
-        shape, stride = t.shape, t.stride()
-        n = len(shape)
-        if n == 3:
-            ok = shape[1] * shape[2] == width and (stride[1] == shape[2] or shape[1] == 1)
-        else:
-            ok = n == 2 and shape[1] == width
-        if not (ok and shape[0] == rows and stride[-1] == 1 and t.dtype is (dtype or self._bf16)
-                and t.get_device() == self._index):
-            raise ValueError(f"{what}: {rows} rows of {width} contiguous {dtype or self._bf16} "
-                             f"elements on cuda:{self._index} are wanted, got shape {tuple(shape)}, "
-                             f"strides {tuple(stride)}, {t.dtype} on {t.device}")
-        return t.data_ptr(), stride[0] if rows > 1 else width
+        shape = t.shape
+        if (t.dtype is (dtype or self._bf16) and t.get_device() == self._index
+                and shape[0] == rows):
+            if t.is_contiguous() and t.numel() == rows * width:
+                return t.data_ptr(), width
+            stride, n = t.stride(), len(shape)
+            if n == 3:
+                ok = shape[1] * shape[2] == width and (stride[1] == shape[2] or shape[1] == 1)
+            else:
+                ok = n == 2 and shape[1] == width
+            if ok and stride[-1] == 1:
+                return t.data_ptr(), stride[0] if rows > 1 else width
+        raise ValueError(f"{what}: {rows} rows of {width} contiguous {dtype or self._bf16} "
+                         f"elements on cuda:{self._index} are wanted, got shape {tuple(shape)}, "
+                         f"strides {tuple(t.stride())}, {t.dtype} on {t.device}")
 
     def _stream(self, stream):
         """A cudaStream_t: the given one, or torch's current stream of the pool's
@@ -438,7 +458,13 @@ class KVCache:
         y, ldy = self._rows(Y, "Y", M, N)
         if N > 1 and ldw != K:
             raise ValueError("W must be contiguous")
-        b = self._rows(bias.unsqueeze(0), "bias", 1, N)[0] if bias is not None else None
+        b = None
+        if bias is not None:
+            if (bias.dtype is not self._bf16 or bias.get_device() != self._index
+                    or bias.numel() != N or not bias.is_contiguous()):
+                raise ValueError(f"bias: {N} contiguous {self._bf16} elements on "
+                                 f"cuda:{self._index} are wanted")
+            b = bias.data_ptr()
         r, ldr = self._rows(R, "R", M, N) if R is not None else (None, 0)
         code = ACTIVATIONS[act] if isinstance(act, str) else int(act)
         _check(self.lib.wave_linear_bias(self.h, a, lda, M, K, w, N, b, r, ldr, code, y, ldy,
@@ -476,9 +502,8 @@ class KVCache:
             kh = K.shape[1]
             k, ldk = self._rows(K, "K", rows, kh * d)
             ko, ldko = self._rows(Kout, "Kout", rows, kh * d)
-        spec = RotarySpec(tuple(pairs), base, ROTARY_LAYOUTS[layout], ROTARY_LADDERS[ladder],
-                          bool(inverse))
-        _check(self.lib.wave_rotary(self.h, ctypes.byref(spec), p, rows, q, ldq, qh, qo, ldqo, k,
+        spec = _rotary_spec(tuple(pairs), base, layout, ladder, bool(inverse))
+        _check(self.lib.wave_rotary(self.h, spec, p, rows, q, ldq, qh, qo, ldqo, k,
                                     ldk, kh, ko, ldko, self._stream(stream)))
         return (Qout, Kout) if K is not None else Qout
 

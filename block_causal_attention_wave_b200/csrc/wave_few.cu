@@ -195,6 +195,7 @@ struct SplitParams {
   const uint16_t* resid;
   const uint16_t* bias;
   int64_t ldr, ldy;
+  int32_t wide;
 };
 
 // The four K = 16 steps of a 64-wide slice in one block: low descriptor words
@@ -425,6 +426,7 @@ int split_rows_launch(const wave_kv* kv, const DenseArgs& a, int nf, int splits,
   p.bias = a.bias;
   p.ldr = a.ldr;
   p.ldy = a.ldy;
+  p.wide = wide_rows(a.Y, a.ldy);
   const int tiles = p.n_ftiles * ((a.M + 127) / 128);
   return nf == 64 ? launch_split_act<64>(p, tiles, a.act, s) : launch_split_act<128>(p, tiles, a.act, s);
 }

@@ -65,6 +65,7 @@ struct PairParams {
   const uint16_t* resid;
   const uint16_t* bias;
   int64_t ldr, ldy;
+  int32_t wide;
 };
 
 __device__ __forceinline__ void pair_cluster_sync() {
@@ -346,6 +347,7 @@ int pair_rows_launch(const wave_kv* kv, const DenseArgs& a, int splits, cudaStre
   p.bias = a.bias;
   p.ldr = a.ldr;
   p.ldy = a.ldy;
+  p.wide = wide_rows(a.Y, a.ldy);
   const int cluster = 2 * splits;
   const int ctas = splits > 1 ? p.n_tiles * cluster : 2 * std::min(p.n_tiles, kv->num_sms / 2);
   switch (a.act) {
