@@ -23,7 +23,7 @@
 //     are cut into parts for several clusters each, which leave their (m, l, O')
 //     in the workspace for a second kernel.
 //   - Warps 0..7 are two teams that take every other unit; a warp takes 32 of
-//     the page's 128 keys, for all 16 rows, with its own running maximum, sum
+//     the page's 128 keys, for all rows, with its own running maximum, sum
 //     and O: no exchange between warps until the segment ends.
 //   - Warps 8 and 9 feed one team each, K and V tiles by TMA through a ring of
 //     the team's own (192 KB in flight per SM). A ring that both teams shared
@@ -32,11 +32,19 @@
 //     team's fill of a slot could take it for its own. S = Q K^T and O += P V are m16n8k16 MMAs on fragments read
 //     from shared memory; one token fills one of 16 rows, but at a byte a cycle
 //     a thread the tensor pipe idles either way, and 16 rows cost what one costs.
-//   - Within an MMA the order of the contracted index is free, so a lane's
-//     operand is whole 16-byte vectors of a token's row (d permuted alike in Q
-//     and K; P's key order is that of S), all conflict-free under the swizzle.
+//   - Both products are m16n8k16 MMAs with the cache as the operand of sixteen rows:
+//     S^T = K Q^T (16 keys x 8 query rows) and O^T += V^T P^T (16 d x 8 query
+//     rows), QT = 1 or 2 tiles of query rows. With the queries as the sixteen rows
+//     one token filled one of them: twice the MMAs, exponentials and registers
+//     (32 FP8 units: 50.7 us, this way FP8_US).
+//   - Within an MMA the order of the contracted index, and which d is which row,
+//     are free, so a lane's operand is whole 16-byte vectors of a token's row, all
+//     conflict-free under the swizzle; P is turned into its operand's layout by
+//     one movmatrix per 8 keys.
 //   - FP8 tiles: codes are exact in f16, so both MMAs run in f16 on converted
-//     codes. Q is scaled by a power of two per row to fit f16 (its 8 bits of
+//     codes (e4m3 MMAs on the codes themselves, with Q and P as sums of two E4M3
+//     values, took 80 us for those 50: this GPU has no fast form of them outside
+//     tcgen05). Q is scaled by a power of two per row to fit f16 (its 8 bits of
 //     mantissa stay exact down to 2^-24 of the row's largest value). P, in
 //     [0, 1], is scaled by 2^15, so what f16 drops is below 2^-39; V's scale is
 //     applied to each page's product in fp32.
@@ -131,8 +139,8 @@ struct TokCfg {
   static constexpr int kRow = D + 4;
   static constexpr int kCtaOff = kTokWarps * kTokRows * kRow * 4;
   static_assert(kCtaOff + kTokRows * kRow * 4 <= kStatOff, "the joins reuse the ring");
-  static constexpr int kTiles = D / 8;    // n-tiles of O
-  static constexpr int kSteps = D / 16;   // k-steps of Q K^T
+  static constexpr int kTiles = D / 16;   // tiles of 16 d of O^T
+  static constexpr int kSteps = D / 16;   // k-steps of K Q^T
 };
 
 template <bool F16>
@@ -191,14 +199,20 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kTokWarps) : "memory");
 }
 
-// d of column c (0, 1) of n-tile t in lane quarter q of O's fragment.
+// First d of the two that lane row r holds of O^T's tile t (the next tile's follow).
 template <int D, bool FP8>
-__device__ __forceinline__ int tok_col(int t, int q, int c) {
-  if (!FP8) return 64 * (t >> 3) + 16 * q + 8 * c + (t & 7);
-  return D == 128 ? 32 * q + 16 * c + t : 16 * q + 8 * c + t;
+__device__ __forceinline__ int tok_d(int t, int r) {
+  if (!FP8) return 64 * (t >> 2) + 8 * r + 2 * (t & 3);
+  return (D == 128 ? 16 : 8) * r + 2 * t;
+}
+// 8 x 8 values of 16 bits, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
-template <int D, bool FP8, int CAP>
+template <int D, bool FP8, int QT, int CAP>
 __global__ void __launch_bounds__(kTokThreads, 1)
     token_attn_kernel(const __grid_constant__ TokParams<CAP> p) {
   using C = TokCfg<D, FP8>;
@@ -279,22 +293,26 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   {
   // ---- consumers: keys 32 (warp % 4) .. + 31 of every other page
   const int key0 = 32 * (warp % kTokTeam);
-  const int r8 = lane >> 2, q4 = lane & 3;   // fragment row (and column group), lane quarter
-  float o[C::kTiles][4];
-  uint32_t qa[C::kSteps][4];
-  float m[2], l[2], qs[2];   // rows r8 and r8 + 8: maximum (log2), this lane's sum, score factor
+  const int r8 = lane >> 2, q4 = lane & 3;   // fragment row, lane quarter
+  float o[QT][C::kTiles][4];                 // O^T: d tok_d + (c >> 1), query row 8 t + 2 q4 + (c & 1)
+  uint32_t qf[QT][C::kSteps][2];             // Q of query row 8 t + r8
+  float m[QT][2], l[QT][2], qs[QT][2];       // of query rows 8 t + 2 q4 (+ 1): maximum (log2), this
+                                             // lane's part of the sum, score factor
   bool dead = false;
   const int rows = grp.rows;
   const uint32_t all_rows = (1u << rows) - 1;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = r8 + 8 * i;
+    for (int t = 0; t < QT; ++t) {
+      const int row = 8 * t + r8;
       const uint16_t* src = h.q + (grp.q0 + row / h.per_kv) * h.ldq +
                             (int64_t)(head * h.per_kv + row % h.per_kv) * D;
       const bool in = row < rows;
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-      qs[i] = h.scale_log2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[t][i] = -INFINITY;
+        l[t][i] = 0.f;
+        qs[t][i] = h.scale_log2;
+      }
       if constexpr (!FP8) {
 #pragma unroll
         for (int b = 0; b < D / 64; ++b)
@@ -303,10 +321,10 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             uint4 v = make_uint4(0, 0, 0, 0);
             if (in) v = *reinterpret_cast<const uint4*>(src + 64 * b + 8 * (2 * q4 + hh));
             const int st = (b * 2 + hh) * 2;
-            qa[st][i] = v.x;
-            qa[st][2 + i] = v.y;
-            qa[st + 1][i] = v.z;
-            qa[st + 1][2 + i] = v.w;
+            qf[t][st][0] = v.x;
+            qf[t][st][1] = v.y;
+            qf[t][st + 1][0] = v.z;
+            qf[t][st + 1][1] = v.w;
           }
       } else {
         // Lane quarter q4 holds d = 16 (D / 64 q4 + hh) .. + 15, hh < D / 64.
@@ -334,120 +352,138 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         if (top > 0.f && top < INFINITY)
           e = min(13 - ((int)(__float_as_uint(top) >> 23) - 127), 120);
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        qs[i] *= __uint_as_float((uint32_t)(127 - e) << 23);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) qs[t][i] *= __shfl_sync(0xffffffffu, down, 8 * q4 + 4 * i);
 #pragma unroll
         for (int st = 0; st < C::kSteps; ++st)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t v = raw[st * 2 + j];
-            qa[st][2 * j + i] = pack_f16x2(__uint_as_float(v << 16) * up,
-                                           __uint_as_float(v & 0xFFFF0000u) * up);
+            qf[t][st][j] = pack_f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
           }
       }
+#pragma unroll
+      for (int x = 0; x < C::kTiles; ++x)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[t][x][c] = 0.f;
     }
-#pragma unroll
-    for (int t = 0; t < C::kTiles; ++t)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) o[t][c] = 0.f;
 
-    // One unit: S = Q K^T, the softmax's step, O += P V, for the warp's 32 keys.
-    // false: a wait ran out. WHOLE: every row sees all 128 tokens.
+    // One unit: S^T = K Q^T, the softmax's step, O^T += V^T P^T, for the warp's 32
+    // keys. false: a wait ran out. WHOLE: every row sees all 128 tokens.
     auto unit = [&](auto whole_c, int ks, int vs, int vp, int seen, uint32_t mask, float sk, float sv) -> bool {
       constexpr bool WHOLE = decltype(whole_c)::value;
       const bool some = WHOLE || key0 < seen;   // the warp has a key that is seen
-      uint32_t pa[2][4];               // P of the warp's two blocks of sixteen keys
-      const bool part[2] = {(mask >> r8 & 1) != 0, (mask >> (r8 + 8) & 1) != 0};
+      uint32_t pb[QT][2][2];                    // P^T of the warp's two blocks of sixteen keys
+      auto sees = [&](int t, int i) { return (mask >> (8 * t + 2 * q4 + i) & 1) != 0; };
       if (some) {
         const uint32_t kt = ring + ks * C::kTile;
-        // ---- S = Q K^T, n-tiles of 8 keys
-        float sc[4][4];
+        // ---- S^T: block kb, keys r8 (c = 0, 1) and r8 + 8 (c = 2, 3)
+        float sc[QT][2][4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int t = 0; t < QT; ++t)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sc[t][kb][c] = 0.f;
         if constexpr (!FP8) {
 #pragma unroll
           for (int b = 0; b < D / 64; ++b)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-              for (int nt = 0; nt < 4; ++nt) {
-                const uint32_t row = kt + b * 16384 + (key0 + nt * 8 + r8) * 128;
-                const uint4 v = lds128(row + (((2 * q4 + hh) ^ r8) << 4));
+              for (int kb = 0; kb < 2; ++kb) {
+                const uint32_t row = kt + b * 16384 + (key0 + kb * 16 + r8) * 128 + (((2 * q4 + hh) ^ r8) << 4);
+                const uint4 u = lds128(row), v = lds128(row + 8 * 128);
+                const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
                 const int st = (b * 2 + hh) * 2;
-                tok_mma<false>(sc[nt], qa[st], v.x, v.y);
-                tok_mma<false>(sc[nt], qa[st + 1], v.z, v.w);
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                  tok_mma<false>(sc[t][kb], a0, qf[t][st][0], qf[t][st][1]);
+                  tok_mma<false>(sc[t][kb], a1, qf[t][st + 1][0], qf[t][st + 1][1]);
+                }
               }
         } else {
 #pragma unroll
           for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-              const int key = key0 + nt * 8 + r8;
-              const int line = D == 128 ? key : key >> 1;
-              const int chunk = D == 128 ? 2 * q4 + hh : (key & 1) * 4 + q4;
-              const uint4 v = lds128(kt + line * 128 + ((chunk ^ (line & 7)) << 4));
-              const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+            for (int kb = 0; kb < 2; ++kb) {
+              uint32_t wd[2][4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                tok_mma<true>(sc[nt], qa[hh * 4 + j], e4m3_f16x2(wd[j] & 0xFFFF), e4m3_f16x2(wd[j] >> 16));
-            }
-        }
-        // ---- softmax of this warp's keys; rows r8 (c = 0, 1) and r8 + 8 (c = 2, 3)
-        float top[2] = {-INFINITY, -INFINITY}, shift[2];
-        const float f0 = FP8 ? qs[0] * sk : qs[0], f1 = FP8 ? qs[1] * sk : qs[1];
+              for (int k = 0; k < 2; ++k) {
+                const int key = key0 + kb * 16 + k * 8 + r8;
+                const int line = D == 128 ? key : key >> 1;
+                const int chunk = D == 128 ? 2 * q4 + hh : (key & 1) * 4 + q4;
+                const uint4 v = lds128(kt + line * 128 + ((chunk ^ (line & 7)) << 4));
+                wd[k][0] = v.x; wd[k][1] = v.y; wd[k][2] = v.z; wd[k][3] = v.w;
+              }
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t a[4] = {e4m3_f16x2(wd[0][j] & 0xFFFF), e4m3_f16x2(wd[1][j] & 0xFFFF),
+                                       e4m3_f16x2(wd[0][j] >> 16), e4m3_f16x2(wd[1][j] >> 16)};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) sc[nt][c] *= c < 2 ? f0 : f1;
-        if (!WHOLE) {
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (!part[c >> 1] || key0 + nt * 8 + 2 * q4 + (c & 1) >= seen) sc[nt][c] = -INFINITY;
-        }
-        bool grew = false;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt) top[i] = fmax3(top[i], sc[nt][2 * i], sc[nt][2 * i + 1]);
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-          top[i] = fmaxf(top[i], m[i]);
-          grew |= top[i] > m[i];
-          shift[i] = top[i] == -INFINITY ? 0.f : top[i];
-        }
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (top[i] > m[i]) {
-              const float f = ex2_approx(m[i] - shift[i]);
-              l[i] *= f;
-              m[i] = top[i];
-#pragma unroll
-              for (int t = 0; t < C::kTiles; ++t) {
-                o[t][2 * i] *= f;
-                o[t][2 * i + 1] *= f;
+                for (int t = 0; t < QT; ++t) tok_mma<true>(sc[t][kb], a, qf[t][hh * 4 + j][0], qf[t][hh * 4 + j][1]);
               }
             }
-          }
         }
+        // ---- softmax of this warp's keys; query rows 2 q4 (c = 0, 2) and 2 q4 + 1 (c = 1, 3)
+        bool grew = false;
+        float top[QT][2], shift[QT][2];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int t = 0; t < QT; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float a = ex2_approx(sc[nt][2 * i] - shift[i]);
-            const float b = ex2_approx(sc[nt][2 * i + 1] - shift[i]);
-            l[i] += a + b;
-            pa[nt >> 1][2 * (nt & 1) + i] = FP8 ? pack_f16x2(a * 32768.f, b * 32768.f) : pack_bf16x2(a, b);
+            const float f = FP8 ? qs[t][i] * sk : qs[t][i];
+            top[t][i] = -INFINITY;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float& x = sc[t][kb][2 * k + i];
+                x *= f;
+                if (!WHOLE && (!sees(t, i) || key0 + kb * 16 + k * 8 + r8 >= seen)) x = -INFINITY;
+                top[t][i] = fmaxf(top[t][i], x);
+              }
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) top[t][i] = fmaxf(top[t][i], __shfl_xor_sync(0xffffffffu, top[t][i], x));
+            top[t][i] = fmaxf(top[t][i], m[t][i]);
+            grew |= top[t][i] > m[t][i];
+            shift[t][i] = top[t][i] == -INFINITY ? 0.f : top[t][i];
           }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int t = 0; t < QT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (top[t][i] > m[t][i]) {
+                const float f = ex2_approx(m[t][i] - shift[t][i]);
+                l[t][i] *= f;
+                m[t][i] = top[t][i];
+#pragma unroll
+                for (int x = 0; x < C::kTiles; ++x) {
+                  o[t][x][i] *= f;
+                  o[t][x][2 + i] *= f;
+                }
+              }
+        }
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float a = ex2_approx(sc[t][kb][2 * k] - shift[t][0]);
+              const float b = ex2_approx(sc[t][kb][2 * k + 1] - shift[t][1]);
+              l[t][0] += a;
+              l[t][1] += b;
+              pb[t][kb][k] = transpose8(FP8 ? pack_f16x2(a * 32768.f, b * 32768.f) : pack_bf16x2(a, b));
+            }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(ks));
       if (!__all_sync(0xffffffffu, wait_bar(full(vs), vp, ctl, 0x403))) return false;
       if (some) {
-        // ---- O += P V: of each block, a lane's keys are 2 q4, + 1, + 8, + 9
+        // ---- O^T += V^T P^T: of each block, a lane's keys are 2 q4, + 1, + 8, + 9
         const uint32_t vt = ring + vs * C::kTile;
         auto key_of = [&](int kb, int k) { return key0 + 16 * kb + 2 * q4 + (k & 1) + 8 * (k >> 1); };
         if constexpr (!FP8) {
@@ -464,18 +500,20 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
               }
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
-                const uint32_t b0 = __byte_perm(x[0][e >> 1], x[1][e >> 1], sel);
-                const uint32_t b1 = __byte_perm(x[2][e >> 1], x[3][e >> 1], sel);
-                float (&acc)[4] = o[b * 8 + e];
-                if (WHOLE) {
-                  tok_mma<false>(acc, pa[kb], b0, b1);
-                } else {
-                  float d[4] = {acc[0], acc[1], acc[2], acc[3]};
-                  tok_mma<false>(d, pa[kb], b0, b1);
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t a[4] = {__byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[0][e], x[1][e], 0x7632),
+                                       __byte_perm(x[2][e], x[3][e], 0x5410), __byte_perm(x[2][e], x[3][e], 0x7632)};
 #pragma unroll
-                  for (int c = 0; c < 4; ++c) acc[c] = part[c >> 1] ? d[c] : acc[c];
+                for (int t = 0; t < QT; ++t) {
+                  float (&acc)[4] = o[t][b * 4 + e];
+                  if (WHOLE) {
+                    tok_mma<false>(acc, a, pb[t][kb][0], pb[t][kb][1]);
+                  } else {
+                    float d[4] = {acc[0], acc[1], acc[2], acc[3]};
+                    tok_mma<false>(d, a, pb[t][kb][0], pb[t][kb][1]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[c] = sees(t, c & 1) ? d[c] : acc[c];
+                  }
                 }
               }
             }
@@ -506,21 +544,21 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             for (int half = 0; half < 2; ++half) {
               // codes of d 4 j + 2 half (low 16 bits) and the next: keys (0, 1) and (8, 9)
               const uint32_t sel = half ? 0x7362 : 0x5140;
-              float d[2][4] = {};
+              float d[QT][4] = {};
 #pragma unroll
               for (int kb = 0; kb < 2; ++kb) {
                 const uint32_t k01 = __byte_perm(x[kb][0][j], x[kb][1][j], sel);
                 const uint32_t k89 = __byte_perm(x[kb][2][j], x[kb][3][j], sel);
-                tok_mma<true>(d[0], pa[kb], e4m3_f16x2(k01 & 0xFFFF), e4m3_f16x2(k89 & 0xFFFF));
-                tok_mma<true>(d[1], pa[kb], e4m3_f16x2(k01 >> 16), e4m3_f16x2(k89 >> 16));
+                const uint32_t a[4] = {e4m3_f16x2(k01 & 0xFFFF), e4m3_f16x2(k01 >> 16), e4m3_f16x2(k89 & 0xFFFF),
+                                       e4m3_f16x2(k89 >> 16)};
+#pragma unroll
+                for (int t = 0; t < QT; ++t) tok_mma<true>(d[t], a, pb[t][kb][0], pb[t][kb][1]);
               }
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float (&acc)[4] = o[4 * j + 2 * half + e];
+              for (int t = 0; t < QT; ++t)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                  if (WHOLE || part[c >> 1]) acc[c] = fmaf(f, d[e][c], acc[c]);
-              }
+                  if (WHOLE || sees(t, c & 1)) o[t][2 * j + half][c] = fmaf(f, d[t][c], o[t][2 * j + half][c]);
             }
         }
       }
@@ -566,29 +604,30 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
     float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (q4 == 0) stat[warp * kTokRows + r8 + 8 * i] = make_float2(m[i], l[i]);
-    }
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], x);
+        if (r8 == 0) stat[warp * kTokRows + 8 * t + 2 * q4 + i] = make_float2(m[t][i], l[t][i]);
+      }
     consumers_sync();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = r8 + 8 * i;
-      if (row >= rows) continue;
-      float top = -INFINITY;
+    for (int t = 0; t < QT; ++t)
 #pragma unroll
-      for (int k = 0; k < kTokWarps; ++k) top = fmaxf(top, stat[k * kTokRows + row].x);
-      const float fac = ex2_approx(m[i] - (top == -INFINITY ? 0.f : top));
-      float* dst = red + (warp * kTokRows + row) * C::kRow;
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * t + 2 * q4 + i;
+        if (row >= rows) continue;
+        float top = -INFINITY;
 #pragma unroll
-      for (int t = 0; t < C::kTiles; t += 4)
+        for (int k = 0; k < kTokWarps; ++k) top = fmaxf(top, stat[k * kTokRows + row].x);
+        const float fac = ex2_approx(m[t][i] - (top == -INFINITY ? 0.f : top));
+        float* dst = red + (warp * kTokRows + row) * C::kRow;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<float4*>(dst + tok_col<D, FP8>(t, q4, c)) =
-              make_float4(o[t][2 * i + c] * fac, o[t + 1][2 * i + c] * fac, o[t + 2][2 * i + c] * fac,
-                          o[t + 3][2 * i + c] * fac);
-    }
+        for (int x = 0; x < C::kTiles; x += 2)
+          *reinterpret_cast<float4*>(dst + tok_d<D, FP8>(x, r8)) =
+              make_float4(o[t][x][i] * fac, o[t][x][2 + i] * fac, o[t][x + 1][i] * fac, o[t][x + 1][2 + i] * fac);
+      }
     consumers_sync();
     float* cta = reinterpret_cast<float*>(smem + C::kCtaOff);
     for (int x = threadIdx.x; x < rows * D; x += 32 * kTokWarps) {
@@ -686,17 +725,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) token_join_kernel(const __gri
     h.lse[at] = mx == -INFINITY ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
 }
 
-template <int D, bool FP8, int CAP>
+template <int D, bool FP8, int QT, int CAP>
 int launch_token(const TokParams<CAP>& p, cudaStream_t s) {
   using C = TokCfg<D, FP8>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   static int regs = 0;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(token_attn_kernel<D, FP8, CAP>,
+    attr_err = cudaFuncSetAttribute(token_attn_kernel<D, FP8, QT, CAP>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     cudaFuncAttributes fa;
-    if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, token_attn_kernel<D, FP8, CAP>);
+    if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, token_attn_kernel<D, FP8, QT, CAP>);
     if (attr_err == cudaSuccess) regs = fa.numRegs;
   });
   if (attr_err != cudaSuccess)
@@ -717,17 +756,21 @@ int launch_token(const TokParams<CAP>& p, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = p.h.cluster > 1 ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, token_attn_kernel<D, FP8, CAP>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, token_attn_kernel<D, FP8, QT, CAP>, p);
   if (e != cudaSuccess) cudaGetLastError();
   if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "token_attn_kernel launch: %s", cudaGetErrorString(e));
   return WAVE_OK;
 }
 
-template <int CAP>
+template <int QT, int CAP>
 int launch_token_any(const wave_kv* kv, const TokParams<CAP>& p, cudaStream_t s) {
   if (kv->cfg.head_dim == 128)
-    return kv->fp8 ? launch_token<128, true, CAP>(p, s) : launch_token<128, false, CAP>(p, s);
-  return kv->fp8 ? launch_token<64, true, CAP>(p, s) : launch_token<64, false, CAP>(p, s);
+    return kv->fp8 ? launch_token<128, true, QT, CAP>(p, s) : launch_token<128, false, QT, CAP>(p, s);
+  return kv->fp8 ? launch_token<64, true, QT, CAP>(p, s) : launch_token<64, false, QT, CAP>(p, s);
+}
+template <int CAP>
+int launch_token_rows(const wave_kv* kv, const TokParams<CAP>& p, cudaStream_t s) {
+  return p.h.rows_max <= 8 ? launch_token_any<1>(kv, p, s) : launch_token_any<2>(kv, p, s);
 }
 
 // CTAs per list (a cluster) and clusters per list for lists of at most `longest`
@@ -928,9 +971,9 @@ extern "C" int wave_token_attn(wave_kv* kv, const wave_node* active, int32_t n_a
     std::memcpy(&small.h, &h, sizeof h);
     std::memcpy(small.page, t.p.page, items * sizeof(uint32_t));
     std::memcpy(small.mask, t.p.mask, items * sizeof(uint16_t));
-    rc = launch_token_any(kv, small, s);
+    rc = launch_token_rows(kv, small, s);
   } else {
-    rc = launch_token_any(kv, t.p, s);
+    rc = launch_token_rows(kv, t.p, s);
   }
   if (rc || h.parts == 1) return rc;
   // The second kernel's launch overlaps the first's end (its blocks wait for it).
