@@ -279,30 +279,21 @@ int device_init(wave_kv* kv) {
   e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
 
-  // Tensor map over the page region, with the 128-byte swizzle: rows of
-  // head_dim bf16, box 64 x 128, as the tensor-core shared-memory descriptors
-  // expect; FP8 pools (which the round's attention reads through bf16 staging
-  // pages) rows of 128 codes, box 128 x d: one (page, K or V, head) tile.
+  // Tensor map over the page region: rows of head_dim bf16, box 64 x 128 with
+  // the 128-byte swizzle the tensor-core shared-memory descriptors expect.
+  // (FP8 pools are read through bf16 staging pages; they need none.)
+  if (kv->fp8) return WAVE_OK;
   auto encode = tensor_map_encoder();
   if (!encode) return fail(WAVE_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
   const int d = kv->cfg.head_dim, H = kv->cfg.heads;
-  const int64_t tiles = (int64_t)kv->max_pages * 2 * H;
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)tiles * kPageTokens};
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)kv->max_pages * 2 * H * kPageTokens};
   cuuint64_t strides[1] = {(cuuint64_t)d * 2};
   cuuint32_t box[2] = {64, 128};
   cuuint32_t estr[2] = {1, 1};
-  if (kv->fp8) {
-    dims[0] = 128;
-    dims[1] = (cuuint64_t)tiles * d;
-    strides[0] = 128;
-    box[0] = 128;
-    box[1] = (cuuint32_t)d;
-  }
   void* base = static_cast<uint8_t*>(kv->cfg.pool) + kv->data_offset;
-  CUresult r = encode(&kv->tm_kv, kv->fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                      2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = encode(&kv->tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box,
+                      estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(WAVE_ERR_CUDA, "cuTensorMapEncodeTiled(pool) failed: %d", (int)r);
   return WAVE_OK;
 }

@@ -30,7 +30,7 @@
 #include "ptx.cuh"
 #include "wave_dense.cuh"
 #include "wave_internal.h"
-#include "wave_sync.cuh"
+#include "wave_wait.cuh"
 
 using namespace wptx;
 
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
       int s = 0;
       uint32_t ph = 1;
       for (int k = k0; k < k1; ++k, ++n) {
-        if (n >= S && !wait_bar_fast(bar(C::kEmpty + s), ph, ctl, 0x501)) break;
+        if (n >= S && !wait_within(bar(C::kEmpty + s), ph, ctl, 0x501)) break;
         mbar_arrive_expect_tx(bar(C::kFull + s), bytes);
         tma_load_2d(sb + s * C::kStage + C::kATile, &p.tm_w, k * 64, ft * NF, bar(C::kFull + s));
         tma_load_2d(sb + s * C::kStage, &p.tm_a, k * 64, mt * 128, bar(C::kFull + s));
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
       int s = 0;
       uint32_t ph = 0;
       for (int n = 0; n < k1 - k0; ++n) {
-        if (!wait_bar_fast(bar(C::kFull + s), ph, ctl, 0x502)) {
+        if (!wait_within(bar(C::kFull + s), ph, ctl, 0x502)) {
           ok = false;
           break;
         }
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
     }
   } else {
     if (p.splits > 1) {
-      __all_sync(0xffffffffu, wait_bar(bar(C::kAccFull), 0, ctl, 0x503));
+      __all_sync(0xffffffffu, wait_within(bar(C::kAccFull), 0, ctl, 0x503));
       tc_fence_after();
     }
   }
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
   if (p.splits == 1) {
     if (warp >= 2)
       finish_row<ACT>(p, trow, (int64_t)mt * 128 + row, ft * NF, 0, NF, row < rows, [&] {
-        const bool ok = __all_sync(0xffffffffu, wait_bar(bar(C::kAccFull), 0, ctl, 0x503));
+        const bool ok = __all_sync(0xffffffffu, wait_within(bar(C::kAccFull), 0, ctl, 0x503));
         tc_fence_after();
         return ok;
       });

@@ -33,7 +33,8 @@ struct wave_kv {
   bool fp8 = false;         // pages hold E4M3 codes with per-(page, head) scales
   int64_t scale_offset = 0; // FP8: byte offset of the scale table in the pool
   alignas(64) CUtensorMap tm_kv;  // rows of d bf16 over every page's K and V
-                                  // (FP8 pools: rows of 128 codes, box 128 x d)
+  alignas(64) CUtensorMap tm_codes;  // FP8 pools: rows of 128 codes, box 128 x d
+  bool codes_mapped = false;         // (made by the first wave_token_attn)
   std::vector<int64_t> page_mark;  // wave_token_attn's host scratch: per page, where
   int64_t mark_gen = 0;            // the list being built has it (see there)
 };

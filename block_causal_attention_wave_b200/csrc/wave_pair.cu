@@ -30,7 +30,7 @@
 #include "ptx.cuh"
 #include "wave_dense.cuh"
 #include "wave_internal.h"
-#include "wave_sync.cuh"
+#include "wave_wait.cuh"
 
 using namespace wptx;
 
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
       for (int t = tile0; t < p.n_tiles && ok; t += tile_step) {
         const int mt = t / p.n_ntiles, nt = t - mt * p.n_ntiles;
         for (int k = k0; k < k1; ++k, ++g) {
-          if (g >= S && !wait_bar_fast(bar(C::kEmpty + s), ph, ctl, 0x601)) {
+          if (g >= S && !wait_within(bar(C::kEmpty + s), ph, ctl, 0x601)) {
             ok = false;
             break;
           }
@@ -205,11 +205,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
       bool ok = true;
       for (int t = tile0; t < p.n_tiles && ok; t += tile_step, ++i) {
         const int acc = i & 1;
-        if (i >= 2 && !wait_bar(bar(C::kAccEmpty + acc), ((i >> 1) - 1) & 1, ctl, 0x602)) break;
+        if (i >= 2 && !wait_within(bar(C::kAccEmpty + acc), ((i >> 1) - 1) & 1, ctl, 0x602)) break;
         tc_fence_after();
         uint32_t accumulate = 0;
         for (int k = k0; k < k1; ++k) {
-          if (!wait_bar_fast(bar(C::kFull + s), ph, ctl, 0x603)) {
+          if (!wait_within(bar(C::kFull + s), ph, ctl, 0x603)) {
             ok = false;
             break;
           }
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
       const int acc = i & 1;
       bool ok = false;
       auto wait = [&] {
-        ok = __all_sync(0xffffffffu, wait_bar(bar(C::kAccFull + acc), (i >> 1) & 1, ctl, 0x604));
+        ok = __all_sync(0xffffffffu, wait_within(bar(C::kAccFull + acc), (i >> 1) & 1, ctl, 0x604));
         tc_fence_after();
         return ok;
       };

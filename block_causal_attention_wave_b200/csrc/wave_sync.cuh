@@ -53,14 +53,6 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ct
   return true;
 }
 
-// The same wait for an issuing thread, whose time between MMAs is the tensor pipe's:
-// one test in line, the rest out of the way. (With the default bounds; short
-// ones go straight to wait_bar.)
-__device__ __forceinline__ bool wait_bar_fast(uint32_t bar, uint32_t parity, const Ctl& ctl, int code) {
-  if (ctl.timeout_ns >= kLongWaitNs && wptx::mbar_try_wait(bar, parity)) return true;
-  return wait_bar(bar, parity, ctl, code);
-}
-
 // Bounded wait that ignores the stop flag: used only while stopping, to let
 // asynchronous copies or MMAs that were already issued complete.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {

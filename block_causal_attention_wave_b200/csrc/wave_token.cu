@@ -22,11 +22,11 @@
 //     clusters that do not pack all 148 cost nothing. Fewer than 8 long lists
 //     are cut into parts for several clusters each, which leave their (m, l, O')
 //     in the workspace for a second kernel.
-//   - Warps 0..7 are two teams that take every other unit; a warp takes 32 of
+//   - Warps are two or three teams that take every other unit; a warp takes 32 of
 //     the page's 128 keys, for all rows, with its own running maximum, sum
 //     and O: no exchange between warps until the segment ends.
-//   - Warps 8 and 9 feed one team each, K and V tiles by TMA through a ring of
-//     the team's own (192 KB in flight per SM). A ring that both teams shared
+//   - A further warp per team feeds it, K and V tiles by TMA through a ring of the
+//     team's own (192 KB in flight per SM in all). A ring that the teams shared
 //     would need every warp at every slot: a parity wait tells apart only the
 //     phase after the last one its waiter saw, so a team that skipped the other
 //     team's fill of a slot could take it for its own. S = Q K^T and O += P V are m16n8k16 MMAs on fragments read
@@ -36,7 +36,7 @@
 //     S^T = K Q^T (16 keys x 8 query rows) and O^T += V^T P^T (16 d x 8 query
 //     rows), QT = 1 or 2 tiles of query rows. With the queries as the sixteen rows
 //     one token filled one of them: twice the MMAs, exponentials and registers
-//     (32 FP8 units: 50.7 us, this way FP8_US).
+//     (32 FP8 units: 50.7 us, this way 40.8).
 //   - Within an MMA the order of the contracted index, and which d is which row,
 //     are free, so a lane's operand is whole 16-byte vectors of a token's row, all
 //     conflict-free under the swizzle; P is turned into its operand's layout by
@@ -69,23 +69,14 @@
 
 #include "ptx.cuh"
 #include "wave_internal.h"
-#include "wave_sync.cuh"
+#include "wave_wait.cuh"
 
 using namespace wptx;
 
 namespace wavei {
 namespace {
 
-constexpr int kTokWarps = 8;                       // consumers
 constexpr int kTokTeam = 4;                        // warps of a unit, 32 keys each
-constexpr int kTokTeams = kTokWarps / kTokTeam;    // unit n of a CTA goes to team n % 2
-// A warpgroup of producers follows, one warp per team and two idle ones: registers
-// move between whole warpgroups.
-constexpr int kTokThreads = 32 * (kTokWarps + 4);
-// d = 128: 168 registers a thread at launch (64,512 of the SM's) become 72 for the
-// producers and 216 for the consumers, 128 * 72 + 256 * 216 = 64,512.
-constexpr int kTokRegsLaunch = 168, kTokRegsFeed = 72, kTokRegsWork = 216;
-static_assert(128 * kTokRegsFeed + 256 * kTokRegsWork <= kTokThreads * kTokRegsLaunch, "register split");
 constexpr int kTokRows = 16;                       // query rows of a group
 
 struct TokGroup {
@@ -126,18 +117,33 @@ struct TokParams {
 constexpr int kTokCapSmall = 512;
 static_assert(sizeof(TokParams<WAVE_MAX_TOKEN_PAGES>) <= 32760, "kernel parameter space is 32 KB");
 
-template <int D, bool FP8>
+template <int D, bool FP8, int QT>
 struct TokCfg {
+  // Unit n of a CTA goes to team n % kTeams. Three teams hide more of the codes'
+  // conversion (12 heads of d = 128 over seven FP8 chunks: 24.7 us, with two 27.7);
+  // bf16 is bound by HBM either way and ends sooner with two (77 own tokens: 6.5
+  // us, with three 7.0).
+  static constexpr int kTeams = FP8 && QT == 1 ? 3 : 2;
+  static constexpr int kWarps = kTokTeam * kTeams;   // consumers
+  // A warpgroup of producers follows, one warp per team and idle ones: registers
+  // move between whole warpgroups.
+  static constexpr int kThreads = 32 * (kWarps + 4);
+  // d = 128: registers a thread at launch, then of producers and consumers: 128 * 72
+  // + 256 * 216 = 64,512 or 128 * 40 + 384 * 152 = 63,488 of the launch's 64,512 or
+  // 65,536.
+  static constexpr int kRegsLaunch = kTeams == 3 ? 128 : 168, kRegsFeed = kTeams == 3 ? 40 : 72,
+                       kRegsWork = kTeams == 3 ? 152 : 216;
+  static_assert(128 * kRegsFeed + 32 * kWarps * kRegsWork <= kThreads * kRegsLaunch, "register split");
   static constexpr int kTile = 128 * D * (FP8 ? 1 : 2);
-  static constexpr int kSlots = 98304 / kTile;                        // of each team's ring
-  static constexpr int kStatOff = kTokTeams * kSlots * kTile;         // [8][16] float2
-  static constexpr int kMlOff = kStatOff + kTokWarps * kTokRows * 8;  // [16] float2: the CTA's
+  static constexpr int kSlots = 196608 / kTeams / kTile;              // of each team's ring
+  static constexpr int kStatOff = kTeams * kSlots * kTile;         // [8][16] float2
+  static constexpr int kMlOff = kStatOff + kWarps * kTokRows * 8;  // [16] float2: the CTA's
   static constexpr int kBarOff = kMlOff + kTokRows * 8;
-  static constexpr int kSmemBytes = kBarOff + 2 * kTokTeams * kSlots * 8 + 16 + 1024;
+  static constexpr int kSmemBytes = kBarOff + 2 * kTeams * kSlots * 8 + 16 + 1024;
   // After the last tile the ring holds the warps' O, [8][16][kRow] fp32, and
   // behind it the CTA's, [16][kRow].
   static constexpr int kRow = D + 4;
-  static constexpr int kCtaOff = kTokWarps * kTokRows * kRow * 4;
+  static constexpr int kCtaOff = kWarps * kTokRows * kRow * 4;
   static_assert(kCtaOff + kTokRows * kRow * 4 <= kStatOff, "the joins reuse the ring");
   static constexpr int kTiles = D / 16;   // tiles of 16 d of O^T
   static constexpr int kSteps = D / 16;   // k-steps of K Q^T
@@ -195,8 +201,9 @@ __device__ __forceinline__ float2 lds_rank2(uint32_t addr, int rank) {
                : "=f"(v.x), "=f"(v.y) : "r"(addr), "r"(rank) : "memory");
   return v;
 }
+template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kTokWarps) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
 // First d of the two that lane row r holds of O^T's tile t (the next tile's follow).
@@ -213,15 +220,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 }
 
 template <int D, bool FP8, int QT, int CAP>
-__global__ void __launch_bounds__(kTokThreads, 1)
+__global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
     token_attn_kernel(const __grid_constant__ TokParams<CAP> p) {
-  using C = TokCfg<D, FP8>;
+  using C = TokCfg<D, FP8, QT>;
   constexpr int S = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_addr(smem);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 16 * kTokTeams * S);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 16 * C::kTeams * S);
   const TokHead& h = p.h;
   const Ctl ctl{abort_flag, h.status, h.wait_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -238,14 +245,14 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   const uint16_t* masks = p.mask + grp.item0;
   // The ring of this warp's team: fill f (K of the team's unit j is fill 2 j, V
   // fill 2 j + 1) is in slot f % S, in phase f / S of its barriers.
-  const int team = warp < kTokWarps ? warp / kTokTeam : warp - kTokWarps;
+  const int team = warp < C::kWarps ? warp / kTokTeam : warp - C::kWarps;
   const uint32_t ring = sb + team * S * C::kTile;
   const uint32_t bars = sb + C::kBarOff + 16u * S * team;
   auto full = [&](int s) -> uint32_t { return bars + 8u * s; };
   auto empty = [&](int s) -> uint32_t { return bars + 8u * (S + s); };
 
   if (threadIdx.x == 0) {
-    for (int t = 0; t < kTokTeams; ++t)
+    for (int t = 0; t < C::kTeams; ++t)
       for (int s = 0; s < S; ++s) {
         mbar_init(sb + C::kBarOff + 16u * S * t + 8u * s, 1);
         mbar_init(sb + C::kBarOff + 16u * S * t + 8u * (S + s), kTokTeam);
@@ -256,17 +263,17 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   }
   __syncthreads();
 
-  if (warp >= kTokWarps) {
-    if constexpr (D == 128) regs_dec<kTokRegsFeed>();
-    if (lane == 0 && team < kTokTeams) {
+  if (warp >= C::kWarps) {
+    if constexpr (D == 128) regs_dec<C::kRegsFeed>();
+    if (lane == 0 && team < C::kTeams) {
       int f = 0;
       bool ok = true;
-      for (int u = u0 + team; u < u1 && ok; u += kTokTeams) {
+      for (int u = u0 + team; u < u1 && ok; u += C::kTeams) {
         const int page = (int)(pages[u] & 0x1FFFFFFu);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const int s = f % S;
-          if (f >= S && !wait_bar(empty(s), (f / S - 1) & 1, ctl, 0x401)) {
+          if (f >= S && !wait_within(empty(s), (f / S - 1) & 1, ctl, 0x401)) {
             ok = false;
             break;
           }
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     // exited): what follows may use more registers than they kept.
     return;
   }
-  if constexpr (D == 128) regs_inc<kTokRegsWork>();
+  if constexpr (D == 128) regs_inc<C::kRegsWork>();
   {
   // ---- consumers: keys 32 (warp % 4) .. + 31 of every other page
   const int key0 = 32 * (warp % kTokTeam);
@@ -481,7 +488,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(ks));
-      if (!__all_sync(0xffffffffu, wait_bar(full(vs), vp, ctl, 0x403))) return false;
+      if (!__all_sync(0xffffffffu, wait_within(full(vs), vp, ctl, 0x403))) return false;
       if (some) {
         // ---- O^T += V^T P^T: of each block, a lane's keys are 2 q4, + 1, + 8, + 9
         const uint32_t vt = ring + vs * C::kTile;
@@ -582,18 +589,18 @@ __global__ void __launch_bounds__(kTokThreads, 1)
       }
     };
     fetch(u0 + team);
-    for (int u = u0 + team; u < u1; u += kTokTeams) {
+    for (int u = u0 + team; u < u1; u += C::kTeams) {
       const int ks = f % S, kp = (f / S) & 1, vs = (f + 1) % S, vp = ((f + 1) / S) & 1;
       f += 2;
       const int seen = (int)(next_word >> 25) + 1;
       const uint32_t mask = next_mask;
       const float sk = next_sk, sv = next_sv;
-      fetch(u + kTokTeams);
-      if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(full(ks), kp, ctl, 0x402));
+      fetch(u + C::kTeams);
+      if (!dead) dead = !__all_sync(0xffffffffu, wait_within(full(ks), kp, ctl, 0x402));
       if (dead) continue;
       // The common unit, of which every row sees every token, has code of its own:
       // with the selections for the others in line (predicated by the compiler)
-      // a unit took 919 instructions a warp instead of WHOLE_COUNT.
+      // a unit took 919 instructions a warp instead of 473 (queries as the sixteen rows).
       const bool whole = seen == kPageTokens && (mask & all_rows) == all_rows;
       if (whole) dead = !unit(std::true_type{}, ks, vs, vp, seen, mask, sk, sv);
       else dead = !unit(std::false_type{}, ks, vs, vp, seen, mask, sk, sv);
@@ -611,7 +618,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         for (int x = 4; x < 32; x *= 2) l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], x);
         if (r8 == 0) stat[warp * kTokRows + 8 * t + 2 * q4 + i] = make_float2(m[t][i], l[t][i]);
       }
-    consumers_sync();
+    consumers_sync<32 * C::kWarps>();
 #pragma unroll
     for (int t = 0; t < QT; ++t)
 #pragma unroll
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         if (row >= rows) continue;
         float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kTokWarps; ++k) top = fmaxf(top, stat[k * kTokRows + row].x);
+        for (int k = 0; k < C::kWarps; ++k) top = fmaxf(top, stat[k * kTokRows + row].x);
         const float fac = ex2_approx(m[t][i] - (top == -INFINITY ? 0.f : top));
         float* dst = red + (warp * kTokRows + row) * C::kRow;
 #pragma unroll
@@ -628,21 +635,21 @@ __global__ void __launch_bounds__(kTokThreads, 1)
           *reinterpret_cast<float4*>(dst + tok_d<D, FP8>(x, r8)) =
               make_float4(o[t][x][i] * fac, o[t][x][2 + i] * fac, o[t][x + 1][i] * fac, o[t][x + 1][2 + i] * fac);
       }
-    consumers_sync();
+    consumers_sync<32 * C::kWarps>();
     float* cta = reinterpret_cast<float*>(smem + C::kCtaOff);
-    for (int x = threadIdx.x; x < rows * D; x += 32 * kTokWarps) {
+    for (int x = threadIdx.x; x < rows * D; x += 32 * C::kWarps) {
       const int row = x / D, d = x % D;
       float sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < kTokWarps; ++k) sum += red[(k * kTokRows + row) * C::kRow + d];
+      for (int k = 0; k < C::kWarps; ++k) sum += red[(k * kTokRows + row) * C::kRow + d];
       cta[row * C::kRow + d] = sum;
     }
     if (threadIdx.x < rows) {
       float top = -INFINITY, den = 0.f;
 #pragma unroll
-      for (int k = 0; k < kTokWarps; ++k) top = fmaxf(top, stat[k * kTokRows + threadIdx.x].x);
+      for (int k = 0; k < C::kWarps; ++k) top = fmaxf(top, stat[k * kTokRows + threadIdx.x].x);
 #pragma unroll
-      for (int k = 0; k < kTokWarps; ++k) {
+      for (int k = 0; k < C::kWarps; ++k) {
         const float2 ml = stat[k * kTokRows + threadIdx.x];
         den += ml.y * ex2_approx(ml.x - (top == -INFINITY ? 0.f : top));
       }
@@ -654,8 +661,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   // run of columns
   __syncwarp();
   if (h.cluster > 1) tok_cluster_sync();
-  else consumers_sync();
-  constexpr int kWorkers = 32 * kTokWarps;
+  else consumers_sync<32 * C::kWarps>();
+  constexpr int kWorkers = 32 * C::kWarps;
   for (int x = rank * kWorkers + threadIdx.x; x < grp.rows * D; x += h.cluster * kWorkers) {
     const int row = x / D, d = x % D;
     const uint32_t at = sb + C::kCtaOff + (uint32_t)(row * C::kRow + d) * 4, ml_at = sb + C::kMlOff + row * 8;
@@ -727,7 +734,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) token_join_kernel(const __gri
 
 template <int D, bool FP8, int QT, int CAP>
 int launch_token(const TokParams<CAP>& p, cudaStream_t s) {
-  using C = TokCfg<D, FP8>;
+  using C = TokCfg<D, FP8, QT>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   static int regs = 0;
@@ -742,12 +749,12 @@ int launch_token(const TokParams<CAP>& p, cudaStream_t s) {
     return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
   // setmaxnreg.inc waits until registers are free: with fewer at launch than the
   // split assumes it would never return.
-  if (D == 128 && regs < kTokRegsLaunch)
+  if (D == 128 && regs < C::kRegsLaunch)
     return fail(WAVE_ERR_UNSUPPORTED, "token_attn_kernel compiled with %d registers per thread; its "
-                "register split needs %d", regs, kTokRegsLaunch);
+                "register split needs %d", regs, C::kRegsLaunch);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.h.n_groups * p.h.heads * p.h.parts * p.h.cluster));
-  cfg.blockDim = dim3(kTokThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr;
@@ -951,7 +958,21 @@ extern "C" int wave_token_attn(wave_kv* kv, const wave_node* active, int32_t n_a
     return fail(WAVE_ERR_ARG, "needs a 256-byte aligned workspace of %llu bytes (got %llu)",
                 (unsigned long long)need, (unsigned long long)workspace_bytes);
   if (int rc = check_current_device(kv)) return rc;
-  h.tm = kv->tm_kv;
+  if (kv->fp8 && !kv->codes_mapped) {
+    auto encode = tensor_map_encoder();
+    if (!encode) return fail(WAVE_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+    cuuint64_t dims[2] = {128, (cuuint64_t)kv->max_pages * 2 * kv->cfg.heads * D};
+    cuuint64_t strides[1] = {128};
+    cuuint32_t box[2] = {128, (cuuint32_t)D};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = encode(&kv->tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                        static_cast<uint8_t*>(kv->cfg.pool) + kv->data_offset, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(WAVE_ERR_CUDA, "cuTensorMapEncodeTiled(codes) failed: %d", (int)r);
+    kv->codes_mapped = true;
+  }
+  h.tm = kv->fp8 ? kv->tm_codes : kv->tm_kv;
   uint8_t* pool = static_cast<uint8_t*>(kv->cfg.pool);
   h.scales = kv->fp8 ? reinterpret_cast<const float*>(pool + kv->scale_offset) : nullptr;
   h.q = static_cast<const uint16_t*>(Q);
