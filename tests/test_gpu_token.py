@@ -38,6 +38,13 @@ def _dev(x):
     return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).cuda().bfloat16()
 
 
+def _dev64(x):
+    """bf16 values by their bits (subnormals too, which a conversion may flush)."""
+    import torch
+    bits = (np.ascontiguousarray(x, dtype=np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    return torch.from_numpy(bits.view(np.int16)).view(torch.bfloat16).cuda()
+
+
 def _strided(x, pad, fill=float("nan")):
     """The same values as columns of a wider tensor (the rest is `fill`)."""
     import torch
@@ -308,6 +315,33 @@ def test_write_fp8_bits(cuda_lib, d, tokens, cuts):
     for i in range(2):
         assert np.array_equal(scales[i], ents[i].scales)
         assert np.array_equal(quant.e4m3_decode(codes[i]), quant.e4m3_decode(ents[i].codes))
+
+
+def test_write_fp8_every_quotient(cuda_lib):
+    """Codes of values that lie on and next to rounding borders: all 128 bf16
+    mantissas over 12 binades, both signs, against a page maximum each from all
+    mantissas, and scales near the ends of float32."""
+    H, d = 2, 128
+    rng = np.random.default_rng(34)
+    mant = 1.0 + np.arange(128) / 128.0
+    for k in range(0, 40):
+        top = mant[(37 * k) % 128] * 2.0 ** rng.integers(-3, 4)
+        if k >= 34:
+            top = (2.0 ** -118, 2.0 ** -125, 2.0 ** -133 * 3, 2.0 ** 110, 2.0 ** 127, 2.0 ** -104 * 1.5)[k - 34]
+        x = np.zeros((100, H, d))
+        vals = mant[None, :] * 2.0 ** -np.arange(0, 100)[:, None] * top
+        x[:] = np.where(rng.random((100, 1, d)) < 0.5, -1, 1) * np.minimum(vals, top)[:, None, :]
+        x[0, :, 0] = top
+        x = oblock.bf16_round(x)
+        kv = _cache(cuda_lib, H, d, 100, 1, pages=1, fp8=True)
+        kv.alloc(0, 1)
+        kv.write_tokens([(0, 1)], [0], _dev64(x), _dev64(x), [100])
+        ent = otok.Fp8Entry(100, H, d)
+        ent.write(0, x)
+        codes, scales = _pages(kv, (0, 1))
+        for i in range(2):
+            assert np.array_equal(scales[i], ent.scales), top
+            assert np.array_equal(codes[i][:, :, :100], ent.codes[:, :, :100]), top
 
 
 # ---------------------------------------------------------- token attention
