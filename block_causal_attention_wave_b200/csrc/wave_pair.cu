@@ -6,11 +6,11 @@
 // What bounds it: the tensor pipe, if the operands arrive. An SM takes in about
 // 60 bytes a clock through TMA; a 128 x 256 tile of one SM wants 48 KB per 512
 // tensor cycles, 96 a clock, so it stops at two thirds. Here a cluster of two
-// CTAs computes a 256 x 256 tile with cta_group::2 MMAs: each CTA holds its own
-// 128 rows of A and half of W's 256 rows, 32 KB per 512 cycles.
+// CTAs computes a 256 x 256 (or 192) tile with cta_group::2 MMAs: each CTA holds its
+// own 128 rows of A and half of W's rows, 32 KB per 512 cycles.
 //
 // How: 74 persistent pairs walk the tiles row-tile-major (A comes from HBM once,
-// the weights stay in L2). Per CTA: warp 0 lane 0 feeds a 6-stage ring by TMA,
+// the weights stay in L2). Per CTA: warp 0 lane 0 feeds a 6- or 7-stage ring by TMA,
 // both CTAs' bytes counted on the even CTA's barrier; warp 1 lane 0 of the even
 // CTA issues the MMAs of both into one of two 256-column TMEM accumulators;
 // warps 2..9 are the epilogue, two warps per 32 rows, while the other accumulator
@@ -38,25 +38,28 @@ namespace wavei {
 namespace {
 
 constexpr int kPairThreads = 320;
-constexpr int kPairStages = 6;
 
+// NT: columns of a tile, 192 or 256 (192 fills the SMs better at some sizes).
+template <int NT>
 struct PairCfg {
-  static constexpr int kATile = 128 * 128;  // 128 rows x 64 bf16, A and W alike
-  static constexpr int kStage = 2 * kATile;
-  static constexpr int kBarOff = kPairStages * kStage;
-  static constexpr int kFull = 0, kEmpty = kPairStages, kAccFull = 2 * kPairStages, kAccEmpty = kAccFull + 2,
+  static constexpr int kATile = 128 * 128;      // 128 rows x 64 bf16
+  static constexpr int kWTile = NT / 2 * 128;   // half of the columns' rows of W
+  static constexpr int kStage = kATile + kWTile;
+  static constexpr int kStages = 204800 / kStage;
+  static constexpr int kBarOff = kStages * kStage;
+  static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2,
                        kDrain = kAccEmpty + 2, kBars = kDrain + 1;
   static constexpr int kSmemBytes = kBarOff + kBars * 8 + 16 + 1024;
-  static constexpr int kPartRow = 256 + 4;  // padded row of a partial tile, as in wave_few.cu
+  static constexpr int kPartRow = NT + 4;  // padded row of a partial tile, as in wave_few.cu
   static_assert(4 * 32 * kPartRow * 4 <= kBarOff && 3 * 43 * kPartRow * 4 <= kBarOff, "partials reuse the ring");
-  // kind::f16, cta_group::2: fp32 accumulate, bf16 A and B, K-major, M = 256, N = 256.
+  // kind::f16, cta_group::2: fp32 accumulate, bf16 A and B, K-major, M = 256, N = NT.
   static constexpr uint32_t kIdesc =
-      (1u << 4) | (1u << 7) | (1u << 10) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
+      (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) | ((256u >> 4) << 24);
 };
 
 struct PairParams {
   CUtensorMap tm_a;  // A [M][K], box 64 x 128
-  CUtensorMap tm_w;  // W [N][K], box 64 x 128
+  CUtensorMap tm_w;  // W [N][K], box 64 x NT / 2
   int32_t* status;
   uint64_t wait_ns;
   int32_t k_slices, n_ntiles, n_tiles, splits;
@@ -114,10 +117,10 @@ __device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask) {
 __device__ __forceinline__ void arrive_rank(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-template <int ACT, bool SPLIT>
+template <int NT, int ACT, bool SPLIT>
 __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid_constant__ PairParams p) {
-  using C = PairCfg;
-  constexpr int S = kPairStages;
+  using C = PairCfg<NT>;
+  constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
           const uint32_t a = sb + s * C::kStage;
           if (half == 0) mbar_arrive_expect_tx(bar(C::kFull + s), 2 * C::kStage);
           tma_load_pair(a, &p.tm_a, k * 64, mt * 256 + half * 128, full0 + 8u * s);
-          tma_load_pair(a + C::kATile, &p.tm_w, k * 64, nt * 256 + half * 128, full0 + 8u * s);
+          tma_load_pair(a + C::kATile, &p.tm_w, k * 64, nt * NT + half * (NT / 2), full0 + 8u * s);
           if (++s == S) s = 0, ph ^= 1;
         }
       }
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
       drain_wait(bar(C::kDrain), 0);
     }
   } else {
-    // Warps w and w + 4 own rows 32 (w % 4) .. (TMEM lanes) and 128 columns each.
+    // Warps w and w + 4 own rows 32 (w % 4) .. (TMEM lanes) and half the columns each.
     const int quarter = warp & 3, side = (warp - 2) >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
       } else {
         const int mt = t / p.n_ntiles, nt = t - mt * p.n_ntiles;
         const int64_t m = (int64_t)mt * 256 + half * 128 + row;
-        finish_row<ACT>(p, trow + 256 * acc, m, nt * 256, 128 * side, 128 * side + 128, m < p.M, wait);
+        finish_row<ACT>(p, trow + 256 * acc, m, nt * NT, NT / 2 * side, NT / 2 * (side + 1), m < p.M, wait);
         if (!ok) break;
         tc_fence_before();
         __syncwarp();
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
     // o * per .., from the same half of every pair, as [pair][row][kPartRow].
     const int mt = tile0 / p.n_ntiles, nt = tile0 - mt * p.n_ntiles;
     const int rows = max(0, min(128, p.M - mt * 256 - half * 128));
-    const int cols = min(256, p.N - nt * 256);
+    const int cols = min(NT, p.N - nt * NT);
     const int per = max(1, (rows + p.splits - 1) / p.splits);
     pair_cluster_sync();  // every CTA of the cluster is done with its ring
     if (warp >= 2) {
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
       const uint32_t remote =
           in_rank(sb + (uint32_t)((pair * per + row - owner * per) * C::kPartRow) * 4, 2 * owner + half);
 #pragma unroll 1
-      for (int c = 128 * side; c < min(cols, 128 * side + 128); c += 32) {
+      for (int c = NT / 2 * side; c < min(cols, NT / 2 * (side + 1)); c += 32) {
         uint32_t v[32];
         tmem_ld32_wait(trow + c, v);
         if (row < rows) {
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
     __syncwarp();
     sum_tiles<ACT, kPairThreads>(p, reinterpret_cast<const float*>(smem), p.splits, per, C::kPartRow,
                                  min(per, rows - pair * per), cols, (int64_t)mt * 256 + half * 128 + pair * per,
-                                 nt * 256, [] { __syncwarp(); pair_cluster_sync(); });
+                                 nt * NT, [] { __syncwarp(); pair_cluster_sync(); });
   }
   __syncwarp();
   tc_fence_before();
@@ -297,20 +300,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
   }
 }
 
-template <int ACT, bool SPLIT>
+template <int NT, int ACT, bool SPLIT>
 int launch_pair(const PairParams& p, int ctas, int cluster, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(pair_rows_kernel<ACT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    PairCfg::kSmemBytes);
+    attr_err = cudaFuncSetAttribute(pair_rows_kernel<NT, ACT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    PairCfg<NT>::kSmemBytes);
   });
   if (attr_err != cudaSuccess)
     return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = PairCfg::kSmemBytes;
+  cfg.dynamicSmemBytes = PairCfg<NT>::kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -318,7 +321,7 @@ int launch_pair(const PairParams& p, int ctas, int cluster, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, pair_rows_kernel<ACT, SPLIT>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, pair_rows_kernel<NT, ACT, SPLIT>, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return fail(WAVE_ERR_CUDA, "pair_rows_kernel launch: %s", cudaGetErrorString(e));
@@ -326,16 +329,30 @@ int launch_pair(const PairParams& p, int ctas, int cluster, cudaStream_t s) {
   return WAVE_OK;
 }
 
+template <int NT, int ACT>
+int launch_pair_any(const PairParams& p, int ctas, int cluster, cudaStream_t s) {
+  return cluster > 2 ? launch_pair<NT, ACT, true>(p, ctas, cluster, s) : launch_pair<NT, ACT, false>(p, ctas, cluster, s);
+}
+template <int NT>
+int launch_pair_act(const PairParams& p, int act, int ctas, int cluster, cudaStream_t s) {
+  switch (act) {
+    case WAVE_ACT_GELU_TANH: return launch_pair_any<NT, WAVE_ACT_GELU_TANH>(p, ctas, cluster, s);
+    case WAVE_ACT_GELU_ERF: return launch_pair_any<NT, WAVE_ACT_GELU_ERF>(p, ctas, cluster, s);
+    case WAVE_ACT_SILU: return launch_pair_any<NT, WAVE_ACT_SILU>(p, ctas, cluster, s);
+    default: return launch_pair_any<NT, WAVE_ACT_NONE>(p, ctas, cluster, s);
+  }
+}
+
 }  // namespace
 
-int pair_rows_launch(const wave_kv* kv, const DenseArgs& a, int splits, cudaStream_t s) {
+int pair_rows_launch(const wave_kv* kv, const DenseArgs& a, int nt, int splits, cudaStream_t s) {
   PairParams p = {};
   if (int rc = encode_kmajor(&p.tm_a, a.A, a.M, a.K, 128, "A", a.lda)) return rc;
-  if (int rc = encode_kmajor(&p.tm_w, a.W, a.N, a.K, 128, "W")) return rc;
+  if (int rc = encode_kmajor(&p.tm_w, a.W, a.N, a.K, (uint32_t)nt / 2, "W")) return rc;
   p.status = static_cast<int32_t*>(kv->cfg.pool);
   p.wait_ns = wait_limit_ns(kv);
   p.k_slices = (a.K + 63) / 64;
-  p.n_ntiles = (a.N + 255) / 256;
+  p.n_ntiles = (a.N + nt - 1) / nt;
   const int64_t tiles = ((int64_t)a.M + 255) / 256 * p.n_ntiles;
   if (tiles >= (1LL << 28)) return fail(WAVE_ERR_ARG, "M x N too large");
   p.n_tiles = (int32_t)tiles;
@@ -350,20 +367,7 @@ int pair_rows_launch(const wave_kv* kv, const DenseArgs& a, int splits, cudaStre
   p.wide = wide_rows(a.Y, a.ldy);
   const int cluster = 2 * splits;
   const int ctas = splits > 1 ? p.n_tiles * cluster : 2 * std::min(p.n_tiles, kv->num_sms / 2);
-  switch (a.act) {
-    case WAVE_ACT_GELU_TANH:
-      return splits > 1 ? launch_pair<WAVE_ACT_GELU_TANH, true>(p, ctas, cluster, s)
-                        : launch_pair<WAVE_ACT_GELU_TANH, false>(p, ctas, cluster, s);
-    case WAVE_ACT_GELU_ERF:
-      return splits > 1 ? launch_pair<WAVE_ACT_GELU_ERF, true>(p, ctas, cluster, s)
-                        : launch_pair<WAVE_ACT_GELU_ERF, false>(p, ctas, cluster, s);
-    case WAVE_ACT_SILU:
-      return splits > 1 ? launch_pair<WAVE_ACT_SILU, true>(p, ctas, cluster, s)
-                        : launch_pair<WAVE_ACT_SILU, false>(p, ctas, cluster, s);
-    default:
-      return splits > 1 ? launch_pair<WAVE_ACT_NONE, true>(p, ctas, cluster, s)
-                        : launch_pair<WAVE_ACT_NONE, false>(p, ctas, cluster, s);
-  }
+  return nt == 192 ? launch_pair_act<192>(p, a.act, ctas, cluster, s) : launch_pair_act<256>(p, a.act, ctas, cluster, s);
 }
 
 }  // namespace wavei
