@@ -60,6 +60,16 @@ int launch_rows(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+int allow_shared(const void* fn, int bytes, int device, std::atomic<uint64_t>& done) {
+  const bool counted = device >= 0 && device < 64;
+  if (counted && (done.load(std::memory_order_acquire) >> device & 1)) return WAVE_OK;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  if (counted) done.fetch_or(1ull << device, std::memory_order_release);
+  return WAVE_OK;
+}
+
 }  // namespace wavei
 
 using namespace wavei;
@@ -70,8 +80,8 @@ extern "C" int wave_linear_bias(wave_kv* kv, const void* A, int64_t lda, int32_t
   clear_error();
   if (!kv) return fail(WAVE_ERR_ARG, "NULL handle");
   if (!kv->on_device) return fail(WAVE_ERR_ARG, "host-only handle (pool == NULL) cannot launch");
-  if (M < 0 || K < 8 || K % 8 != 0 || K > (1 << 16) || N < 8 || N % 8 != 0 || N > (1 << 16))
-    return fail(WAVE_ERR_ARG, "need M >= 0, K and N positive multiples of 8 (at most 65536); got "
+  if (M < 0 || M > (1 << 30) || K < 8 || K % 8 != 0 || K > (1 << 16) || N < 8 || N % 8 != 0 || N > (1 << 16))
+    return fail(WAVE_ERR_ARG, "need 0 <= M <= 2^30, K and N positive multiples of 8 (at most 65536); got "
                 "M %d, K %d, N %d", M, K, N);
   if ((int64_t)M * N >= (1LL << 40)) return fail(WAVE_ERR_ARG, "M x N too large");
   if (act < WAVE_ACT_NONE || act > WAVE_ACT_SILU) return fail(WAVE_ERR_ARG, "unknown activation %d", act);

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -169,6 +170,11 @@ __device__ __forceinline__ void finish_row(const P& p, uint32_t tmem, int64_t m,
 inline bool wide_rows(const uint16_t* y, int64_t ldy) {
   return (reinterpret_cast<uintptr_t>(y) & 31) == 0 && ldy % 16 == 0;
 }
+
+// Let kernel `fn` use `bytes` of dynamic shared memory on the current device, once
+// per device (an attribute belongs to a device): `done` is the kernel's own word,
+// a bit per device.
+int allow_shared(const void* fn, int bytes, int device, std::atomic<uint64_t>& done);
 
 // A checked call of wave_linear_bias.
 struct DenseArgs {

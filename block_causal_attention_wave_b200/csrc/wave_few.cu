@@ -25,7 +25,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <mutex>
 
 #include "ptx.cuh"
 #include "wave_dense.cuh"
@@ -357,15 +356,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
 }
 
 template <int NF, int ACT>
-int launch_split(const SplitParams& p, int tiles, cudaStream_t s) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(split_rows_kernel<NF, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    SplitCfg<NF>::kSmemBytes);
-  });
-  if (attr_err != cudaSuccess)
-    return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+int launch_split(const SplitParams& p, int tiles, int device, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  if (int rc = allow_shared(reinterpret_cast<const void*>(&split_rows_kernel<NF, ACT>), SplitCfg<NF>::kSmemBytes, device, done)) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * p.splits));
   cfg.blockDim = dim3(kSplitThreads);
@@ -386,12 +379,12 @@ int launch_split(const SplitParams& p, int tiles, cudaStream_t s) {
 }
 
 template <int NF>
-int launch_split_act(const SplitParams& p, int tiles, int act, cudaStream_t s) {
+int launch_split_act(const SplitParams& p, int tiles, int act, int device, cudaStream_t s) {
   switch (act) {
-    case WAVE_ACT_GELU_TANH: return launch_split<NF, WAVE_ACT_GELU_TANH>(p, tiles, s);
-    case WAVE_ACT_GELU_ERF: return launch_split<NF, WAVE_ACT_GELU_ERF>(p, tiles, s);
-    case WAVE_ACT_SILU: return launch_split<NF, WAVE_ACT_SILU>(p, tiles, s);
-    default: return launch_split<NF, WAVE_ACT_NONE>(p, tiles, s);
+    case WAVE_ACT_GELU_TANH: return launch_split<NF, WAVE_ACT_GELU_TANH>(p, tiles, device, s);
+    case WAVE_ACT_GELU_ERF: return launch_split<NF, WAVE_ACT_GELU_ERF>(p, tiles, device, s);
+    case WAVE_ACT_SILU: return launch_split<NF, WAVE_ACT_SILU>(p, tiles, device, s);
+    default: return launch_split<NF, WAVE_ACT_NONE>(p, tiles, device, s);
   }
 }
 
@@ -428,7 +421,8 @@ int split_rows_launch(const wave_kv* kv, const DenseArgs& a, int nf, int splits,
   p.ldy = a.ldy;
   p.wide = wide_rows(a.Y, a.ldy);
   const int tiles = p.n_ftiles * ((a.M + 127) / 128);
-  return nf == 64 ? launch_split_act<64>(p, tiles, a.act, s) : launch_split_act<128>(p, tiles, a.act, s);
+  return nf == 64 ? launch_split_act<64>(p, tiles, a.act, kv->device, s)
+                  : launch_split_act<128>(p, tiles, a.act, kv->device, s);
 }
 
 }  // namespace wavei

@@ -25,7 +25,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <mutex>
 
 #include "ptx.cuh"
 #include "wave_dense.cuh"
@@ -301,15 +300,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
 }
 
 template <int NT, int ACT, bool SPLIT>
-int launch_pair(const PairParams& p, int ctas, int cluster, cudaStream_t s) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(pair_rows_kernel<NT, ACT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    PairCfg<NT>::kSmemBytes);
-  });
-  if (attr_err != cudaSuccess)
-    return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+int launch_pair(const PairParams& p, int ctas, int cluster, int device, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  if (int rc = allow_shared(reinterpret_cast<const void*>(&pair_rows_kernel<NT, ACT, SPLIT>), PairCfg<NT>::kSmemBytes, device, done)) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kPairThreads);
@@ -330,16 +323,17 @@ int launch_pair(const PairParams& p, int ctas, int cluster, cudaStream_t s) {
 }
 
 template <int NT, int ACT>
-int launch_pair_any(const PairParams& p, int ctas, int cluster, cudaStream_t s) {
-  return cluster > 2 ? launch_pair<NT, ACT, true>(p, ctas, cluster, s) : launch_pair<NT, ACT, false>(p, ctas, cluster, s);
+int launch_pair_any(const PairParams& p, int ctas, int cluster, int device, cudaStream_t s) {
+  return cluster > 2 ? launch_pair<NT, ACT, true>(p, ctas, cluster, device, s)
+                     : launch_pair<NT, ACT, false>(p, ctas, cluster, device, s);
 }
 template <int NT>
-int launch_pair_act(const PairParams& p, int act, int ctas, int cluster, cudaStream_t s) {
+int launch_pair_act(const PairParams& p, int act, int ctas, int cluster, int device, cudaStream_t s) {
   switch (act) {
-    case WAVE_ACT_GELU_TANH: return launch_pair_any<NT, WAVE_ACT_GELU_TANH>(p, ctas, cluster, s);
-    case WAVE_ACT_GELU_ERF: return launch_pair_any<NT, WAVE_ACT_GELU_ERF>(p, ctas, cluster, s);
-    case WAVE_ACT_SILU: return launch_pair_any<NT, WAVE_ACT_SILU>(p, ctas, cluster, s);
-    default: return launch_pair_any<NT, WAVE_ACT_NONE>(p, ctas, cluster, s);
+    case WAVE_ACT_GELU_TANH: return launch_pair_any<NT, WAVE_ACT_GELU_TANH>(p, ctas, cluster, device, s);
+    case WAVE_ACT_GELU_ERF: return launch_pair_any<NT, WAVE_ACT_GELU_ERF>(p, ctas, cluster, device, s);
+    case WAVE_ACT_SILU: return launch_pair_any<NT, WAVE_ACT_SILU>(p, ctas, cluster, device, s);
+    default: return launch_pair_any<NT, WAVE_ACT_NONE>(p, ctas, cluster, device, s);
   }
 }
 
@@ -367,7 +361,8 @@ int pair_rows_launch(const wave_kv* kv, const DenseArgs& a, int nt, int splits, 
   p.wide = wide_rows(a.Y, a.ldy);
   const int cluster = 2 * splits;
   const int ctas = splits > 1 ? p.n_tiles * cluster : 2 * std::min(p.n_tiles, kv->num_sms / 2);
-  return nt == 192 ? launch_pair_act<192>(p, a.act, ctas, cluster, s) : launch_pair_act<256>(p, a.act, ctas, cluster, s);
+  return nt == 192 ? launch_pair_act<192>(p, a.act, ctas, cluster, kv->device, s)
+                   : launch_pair_act<256>(p, a.act, ctas, cluster, kv->device, s);
 }
 
 }  // namespace wavei

@@ -61,13 +61,13 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 #include <new>
 #include <type_traits>
 #include <utility>
 #include <vector>
 
 #include "ptx.cuh"
+#include "wave_dense.cuh"
 #include "wave_internal.h"
 #include "wave_wait.cuh"
 
@@ -733,20 +733,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) token_join_kernel(const __gri
 }
 
 template <int D, bool FP8, int QT, int CAP>
-int launch_token(const TokParams<CAP>& p, cudaStream_t s) {
+int launch_token(const TokParams<CAP>& p, int device, cudaStream_t s) {
   using C = TokCfg<D, FP8, QT>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int regs = 0;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(token_attn_kernel<D, FP8, QT, CAP>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<uint64_t> done{0};
+  const void* fn = reinterpret_cast<const void*>(&token_attn_kernel<D, FP8, QT, CAP>);
+  if (int rc = allow_shared(fn, C::kSmemBytes, device, done)) return rc;
+  static const int regs = [fn] {
     cudaFuncAttributes fa;
-    if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, token_attn_kernel<D, FP8, QT, CAP>);
-    if (attr_err == cudaSuccess) regs = fa.numRegs;
-  });
-  if (attr_err != cudaSuccess)
-    return fail(WAVE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+    return cudaFuncGetAttributes(&fa, fn) == cudaSuccess ? fa.numRegs : 0;
+  }();
   // setmaxnreg.inc waits until registers are free: with fewer at launch than the
   // split assumes it would never return.
   if (D == 128 && regs < C::kRegsLaunch)
@@ -772,8 +767,8 @@ int launch_token(const TokParams<CAP>& p, cudaStream_t s) {
 template <int QT, int CAP>
 int launch_token_any(const wave_kv* kv, const TokParams<CAP>& p, cudaStream_t s) {
   if (kv->cfg.head_dim == 128)
-    return kv->fp8 ? launch_token<128, true, QT, CAP>(p, s) : launch_token<128, false, QT, CAP>(p, s);
-  return kv->fp8 ? launch_token<64, true, QT, CAP>(p, s) : launch_token<64, false, QT, CAP>(p, s);
+    return kv->fp8 ? launch_token<128, true, QT, CAP>(p, kv->device, s) : launch_token<128, false, QT, CAP>(p, kv->device, s);
+  return kv->fp8 ? launch_token<64, true, QT, CAP>(p, kv->device, s) : launch_token<64, false, QT, CAP>(p, kv->device, s);
 }
 template <int CAP>
 int launch_token_rows(const wave_kv* kv, const TokParams<CAP>& p, cudaStream_t s) {

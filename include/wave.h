@@ -249,7 +249,7 @@ int wave_linear(wave_kv* kv, const void* A, int32_t M, int32_t K, const void* W,
  * past N are not touched. Y may be R itself (with ldy = ldr); Y may overlap
  * nothing else. Strides are in elements, multiples of 8 and at least the row's
  * length; all pointers are 16-byte aligned; K and N are multiples of 8, K >= 8,
- * N >= 8, K, N <= 65536. M = 0 is allowed and does nothing. `kv` as for
+ * N >= 8, K, N <= 65536, M <= 2^30. M = 0 is allowed and does nothing. `kv` as for
  * wave_linear. Results do not depend on M's other rows, but a row's last bits
  * may differ between small and large M (the sums are split differently).
  * Errors: ARG, CUDA. A device-side timeout is reported by wave_kv_status. */

@@ -80,6 +80,7 @@ int main(int argc, char** argv) {
   expect(lin(p, 64, 3, 64, p, 64, p, p, 64, 3, p, 64), stop, "linear: good arguments reach the device check");
   expect(lin(nullptr, 64, 0, 64, nullptr, 64, nullptr, nullptr, 0, 0, nullptr, 64), WAVE_OK, "linear: no rows");
   expect(lin(p, 64, -1, 64, p, 64, p, p, 64, 0, p, 64), bad, "linear: M < 0");
+  expect(lin(p, 64, (1 << 30) + 1, 64, p, 8, p, p, 64, 0, p, 64), bad, "linear: M > 2^30");
   expect(lin(p, 64, 3, 60, p, 64, p, p, 64, 0, p, 64), bad, "linear: K % 8");
   expect(lin(p, 64, 3, 64, p, 60, p, p, 64, 0, p, 64), bad, "linear: N % 8");
   expect(lin(p, 64, 3, 0, p, 64, p, p, 64, 0, p, 64), bad, "linear: K = 0");

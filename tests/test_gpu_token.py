@@ -682,6 +682,55 @@ def test_token_ops_in_a_graph_on_a_side_stream(cuda_lib):
     del graph
 
 
+@pytest.mark.parametrize("M,K,N", [(40, 4096, 1536), (300, 8960, 1536), (3000, 1536, 4608)],
+                         ids=["cluster", "split pairs", "pairs"])
+def test_linear_timeout_is_reported(cuda_lib, M, K, N):
+    """A wait that runs out in the tiled forms is reported, the cluster leaves in
+    step, and the next call is right again."""
+    import torch
+    kv = _cache(cuda_lib)
+    a = torch.ones(M, K, dtype=torch.bfloat16, device="cuda")
+    w = torch.full((N, K), 2.0 ** -10, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    kv.set_wait_limit(1)
+    kv.linear_bias(a, w, y)
+    with pytest.raises(cuda_lib.WaveError) as e:
+        kv.status()
+    assert e.value.code == -5
+    kv.set_wait_limit(0)
+    kv.linear_bias(a, w, y)
+    kv.status()
+    assert (y == K * 2.0 ** -10).all()   # 4, 8.75 or 1.5: exact in bf16
+
+
+def test_token_attn_two_streams(cuda_lib):
+    """Calls on two streams at once, a workspace each, and one on a third stream
+    with other sizes: the results of calls alone."""
+    import torch
+    w = _World(cuda_lib, 2, 64, 640, 1, pages=200, seed=16)
+    for c in range(30):
+        w.add(c, 1)
+    kv = w.kv
+    cases = [([(29, 1)], [640], 2), ([(28, 1), (29, 1)], [3, 77], 4), ([(5, 1)] * 3, [1, 2, 640], 2)]
+    q = [torch.randn(len(n), g, 64, device="cuda").bfloat16() for n, _, g in cases]
+    ws = [torch.empty(max(1, kv.token_attn_workspace(n, "same", own, q_heads=g)), dtype=torch.uint8, device="cuda")
+          for n, own, g in cases]
+    want = []
+    for (n, own, g), x, s in zip(cases, q, ws):
+        o = torch.empty_like(x)
+        kv.token_attn(n, "same", x, o, own_tokens=own, workspace=s)
+        want.append(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[torch.empty_like(x) for _ in range(20)] for x in q]
+    for i in range(20):
+        for (n, own, g), x, s, o, stream in zip(cases, q, ws, got, streams):
+            kv.token_attn(n, "same", x, o[i], own_tokens=own, workspace=s, stream=stream)
+    torch.cuda.synchronize()
+    for w0, os in zip(want, got):
+        assert all(torch.equal(o, w0) for o in os)
+
+
 def test_token_attn_timeout_is_reported(cuda_lib):
     """A wait that runs out is reported, and the next call is right again. 210 MB
     of pages, so that tiles come from HBM, one every 1.4 us per SM."""
