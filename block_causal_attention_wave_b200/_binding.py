@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libwave.so")
@@ -127,19 +128,18 @@ _SIGS = {
                                    ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                    ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
                                    ctypes.c_int64, ctypes.c_void_p]),
-    "wave_kv_write_tokens": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(Node),
-                                            ctypes.POINTER(ctypes.c_int32),
-                                            ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p,
+    # int32 arrays and nodes of these calls come as bytes (_ints, _pairs)
+    "wave_kv_write_tokens": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                             ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
                                             ctypes.c_void_p]),
-    "wave_token_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(Node), ctypes.c_int32,
-                                       ctypes.c_int32, ctypes.POINTER(ctypes.c_int32),
-                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+    "wave_token_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
-                                       ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]),
-    "wave_token_attn_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(Node),
-                                                 ctypes.c_int32, ctypes.c_int32,
-                                                 ctypes.POINTER(ctypes.c_int32), ctypes.c_int32,
+                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_uint64, ctypes.c_void_p]),
+    "wave_token_attn_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                                 ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
                                                  ctypes.POINTER(ctypes.c_uint64)]),
     "wave_kv_append_batch": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(Node),
                                             ctypes.POINTER(ctypes.c_void_p),
@@ -205,27 +205,24 @@ def _policy(policy) -> int:
     return POLICIES[policy] if isinstance(policy, str) else int(policy)
 
 
-@functools.lru_cache(maxsize=None)
-def _node_array(n):
-    return Node * max(1, n)
-
-
 def _nodes(active):
-    arr = _node_array(len(active))()
-    for a, (c, l) in zip(arr, active):
-        a.chunk, a.level = int(c), int(l)
+    arr = (Node * max(1, len(active)))()
+    for i, (c, l) in enumerate(active):
+        arr[i].chunk, arr[i].level = int(c), int(l)
     return arr
 
 
-@functools.lru_cache(maxsize=None)
-def _int_array(n):
-    return ctypes.c_int32 * max(1, n)
-
-
 def _ints(values, n, what):
+    """int32 values as the bytes a C call reads them from (a fraction of the time a
+    ctypes array takes)."""
     if len(values) != n:
         raise ValueError(f"{what}: {n} values wanted, got {len(values)}")
-    return _int_array(n)(*values)
+    return struct.pack(f"{n}i", *values)
+
+
+def _pairs(active):
+    """(chunk, level) nodes as the bytes of a wave_node array."""
+    return struct.pack(f"{2 * len(active)}i", *[x for c, l in active for x in (c, l)])
 
 
 @functools.lru_cache(maxsize=256)
@@ -412,21 +409,18 @@ class KVCache:
         ``width`` contiguous elements: 2-D [rows][width], or [rows][heads][d]
         with contiguous heads. A kernel would read a host tensor's address, or
         past a short one, as readily as a good one, so both are refused here."""
-        shape = t.shape
-        if (t.dtype is (dtype or self._bf16) and t.get_device() == self._index
-                and shape[0] == rows):
-            if t.is_contiguous() and t.numel() == rows * width:
-                return t.data_ptr(), width
-            stride, n = t.stride(), len(shape)
-            if n == 3:
-                ok = shape[1] * shape[2] == width and (stride[1] == shape[2] or shape[1] == 1)
-            else:
-                ok = n == 2 and shape[1] == width
-            if ok and stride[-1] == 1:
-                return t.data_ptr(), stride[0] if rows > 1 else width
-        raise ValueError(f"{what}: {rows} rows of {width} contiguous {dtype or self._bf16} "
-                         f"elements on cuda:{self._index} are wanted, got shape {tuple(shape)}, "
-                         f"strides {tuple(t.stride())}, {t.dtype} on {t.device}")
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 3:
+            ok = (shape[1] * shape[2] == width and stride[2] == 1
+                  and (stride[1] == shape[2] or shape[1] == 1))
+        else:
+            ok = len(shape) == 2 and shape[1] == width and stride[1] == 1
+        if not (ok and shape[0] == rows and t.dtype is (dtype or self._bf16)
+                and t.get_device() == self._index):
+            raise ValueError(f"{what}: {rows} rows of {width} contiguous {dtype or self._bf16} "
+                             f"elements on cuda:{self._index} are wanted, got shape {tuple(shape)}, "
+                             f"strides {tuple(stride)}, {t.dtype} on {t.device}")
+        return t.data_ptr(), stride[0] if rows > 1 else width
 
     def _stream(self, stream):
         """A cudaStream_t: the given one, or torch's current stream of the pool's
@@ -518,7 +512,7 @@ class KVCache:
         width, rows = self.heads * self.head_dim, sum(counts)
         k, ldk = self._rows(K, "K", rows, width)
         v, ldv = self._rows(V, "V", rows, width)
-        _check(self.lib.wave_kv_write_tokens(self.h, n, _nodes(entries), _ints(first, n, "first"),
+        _check(self.lib.wave_kv_write_tokens(self.h, n, _pairs(entries), _ints(first, n, "first"),
                                              _ints(counts, n, "counts"), k, ldk, v, ldv,
                                              self._stream(stream)))
 
@@ -527,7 +521,7 @@ class KVCache:
         n = len(active)
         own = _ints(own_tokens, n, "own_tokens") if own_tokens is not None else None
         b = ctypes.c_uint64(0)
-        _check(self.lib.wave_token_attn_workspace(self.h, _nodes(active), n, _policy(policy), own,
+        _check(self.lib.wave_token_attn_workspace(self.h, _pairs(active), n, _policy(policy), own,
                                                   q_heads or self.heads, ctypes.byref(b)))
         return b.value
 
@@ -554,7 +548,7 @@ class KVCache:
             if workspace.get_device() != self._index or not workspace.is_contiguous():
                 raise ValueError(f"workspace: a contiguous tensor on cuda:{self._index} is wanted")
             ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        _check(self.lib.wave_token_attn(self.h, _nodes(active), n, _policy(policy), own, q_heads, q,
+        _check(self.lib.wave_token_attn(self.h, _pairs(active), n, _policy(policy), own, q_heads, q,
                                         ldq, o, ldo, s, ws, nbytes, self._stream(stream)))
         return O
 

@@ -61,7 +61,7 @@ struct Eight {
 template <class P>
 __device__ __forceinline__ Eight fetch8(const P& p, int64_t m, int col, bool in) {
   Eight e{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  if (in && p.bias) e.b = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
+  if (in && p.bias) e.b = *reinterpret_cast<const uint4*>(p.bias + col);
   if (in && p.resid) e.r = *reinterpret_cast<const uint4*>(p.resid + m * p.ldr + col);
   return e;
 }

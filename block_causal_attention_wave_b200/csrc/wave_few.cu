@@ -58,7 +58,7 @@ __device__ __forceinline__ uint4 ld_weights(const uint16_t* p, bool in) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
       "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      "@p ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
       : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)in));
   return v;
 }
@@ -67,7 +67,7 @@ __device__ __forceinline__ uint4 ld_rows(const uint16_t* p, bool in) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
       "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
       : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)in));
   return v;
 }
@@ -84,6 +84,8 @@ template <int WARPS, int FT, bool R16, int ACT>
 __global__ void __launch_bounds__(32 * WARPS) token_rows_kernel(const __grid_constant__ TokenRowsParams p) {
   constexpr int U = FT == 1 ? 4 : 2;  // chunks of K in a batch
   __shared__ float red[WARPS][16][8 * FT];
+  chain_begin();
+  chain_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r8 = lane >> 2, q4 = lane & 3;
   const int f0 = blockIdx.x * 8 * FT;
@@ -152,13 +154,18 @@ __global__ void __launch_bounds__(32 * WARPS) token_rows_kernel(const __grid_con
 }
 
 template <int WARPS, int FT, bool R16>
-void launch_token_rows(const TokenRowsParams& p, int act, cudaStream_t s) {
-  const unsigned grid = (unsigned)((p.N + 8 * FT - 1) / (8 * FT));
+cudaError_t launch_token_rows(const TokenRowsParams& p, int act, cudaStream_t s) {
+  const dim3 grid((unsigned)((p.N + 8 * FT - 1) / (8 * FT)));
+  const unsigned threads = 32 * WARPS;
   switch (act) {
-    case WAVE_ACT_GELU_TANH: token_rows_kernel<WARPS, FT, R16, WAVE_ACT_GELU_TANH><<<grid, 32 * WARPS, 0, s>>>(p); break;
-    case WAVE_ACT_GELU_ERF: token_rows_kernel<WARPS, FT, R16, WAVE_ACT_GELU_ERF><<<grid, 32 * WARPS, 0, s>>>(p); break;
-    case WAVE_ACT_SILU: token_rows_kernel<WARPS, FT, R16, WAVE_ACT_SILU><<<grid, 32 * WARPS, 0, s>>>(p); break;
-    default: token_rows_kernel<WARPS, FT, R16, WAVE_ACT_NONE><<<grid, 32 * WARPS, 0, s>>>(p);
+    case WAVE_ACT_GELU_TANH:
+      return launch_chained(token_rows_kernel<WARPS, FT, R16, WAVE_ACT_GELU_TANH>, grid, threads, 0, s, 1, p);
+    case WAVE_ACT_GELU_ERF:
+      return launch_chained(token_rows_kernel<WARPS, FT, R16, WAVE_ACT_GELU_ERF>, grid, threads, 0, s, 1, p);
+    case WAVE_ACT_SILU:
+      return launch_chained(token_rows_kernel<WARPS, FT, R16, WAVE_ACT_SILU>, grid, threads, 0, s, 1, p);
+    default:
+      return launch_chained(token_rows_kernel<WARPS, FT, R16, WAVE_ACT_NONE>, grid, threads, 0, s, 1, p);
   }
 }
 
@@ -258,6 +265,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  chain_begin();
+  chain_wait();
   const int rows = min(128, p.M - mt * 128);   // rows of this tile
   const int cols = min(NF, p.N - ft * NF);     // columns of this tile, a multiple of 8
 
@@ -359,22 +368,10 @@ template <int NF, int ACT>
 int launch_split(const SplitParams& p, int tiles, int device, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   if (int rc = allow_shared(reinterpret_cast<const void*>(&split_rows_kernel<NF, ACT>), SplitCfg<NF>::kSmemBytes, device, done)) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.splits));
-  cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = SplitCfg<NF>::kSmemBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)p.splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, split_rows_kernel<NF, ACT>, p);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
+  const cudaError_t e = launch_chained(split_rows_kernel<NF, ACT>, dim3((unsigned)(tiles * p.splits)), kSplitThreads,
+                                       SplitCfg<NF>::kSmemBytes, s, (unsigned)p.splits, p);
+  if (e != cudaSuccess)
     return fail(WAVE_ERR_CUDA, "split_rows_kernel launch: %s", cudaGetErrorString(e));
-  }
   return WAVE_OK;
 }
 
@@ -394,10 +391,10 @@ int token_rows_launch(const DenseArgs& a, int ft, int warps, cudaStream_t s) {
   const TokenRowsParams p{static_cast<const uint16_t*>(a.A), static_cast<const uint16_t*>(a.W), a.Y, a.R, a.bias,
                           a.lda, a.ldr, a.ldy, a.M, a.K, a.N};
   const bool r16 = a.M > 8;
-  if (warps == 16) launch_token_rows<16, 1, false>(p, a.act, s);
-  else if (ft == 1) r16 ? launch_token_rows<8, 1, true>(p, a.act, s) : launch_token_rows<8, 1, false>(p, a.act, s);
-  else r16 ? launch_token_rows<8, 2, true>(p, a.act, s) : launch_token_rows<8, 2, false>(p, a.act, s);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      warps == 16 ? launch_token_rows<16, 1, false>(p, a.act, s)
+      : ft == 1   ? (r16 ? launch_token_rows<8, 1, true>(p, a.act, s) : launch_token_rows<8, 1, false>(p, a.act, s))
+                  : (r16 ? launch_token_rows<8, 2, true>(p, a.act, s) : launch_token_rows<8, 2, false>(p, a.act, s));
   if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "token_rows_kernel launch: %s", cudaGetErrorString(e));
   return WAVE_OK;
 }

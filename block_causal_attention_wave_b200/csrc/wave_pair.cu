@@ -164,6 +164,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
   pair_cluster_sync();  // every CTA's barriers exist before another CTA signals them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  chain_begin();
+  chain_wait();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -303,22 +305,10 @@ template <int NT, int ACT, bool SPLIT>
 int launch_pair(const PairParams& p, int ctas, int cluster, int device, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   if (int rc = allow_shared(reinterpret_cast<const void*>(&pair_rows_kernel<NT, ACT, SPLIT>), PairCfg<NT>::kSmemBytes, device, done)) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = PairCfg<NT>::kSmemBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, pair_rows_kernel<NT, ACT, SPLIT>, p);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
+  const cudaError_t e = launch_chained(pair_rows_kernel<NT, ACT, SPLIT>, dim3((unsigned)ctas), kPairThreads,
+                                       PairCfg<NT>::kSmemBytes, s, (unsigned)cluster, p);
+  if (e != cudaSuccess)
     return fail(WAVE_ERR_CUDA, "pair_rows_kernel launch: %s", cudaGetErrorString(e));
-  }
   return WAVE_OK;
 }
 

@@ -25,6 +25,7 @@
 
 #include "ptx.cuh"
 #include "wave_internal.h"
+#include "wave_wait.cuh"
 
 namespace wavei {
 namespace {
@@ -51,6 +52,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
                                                                const float sign) {
   constexpr int kPairs = HALVES ? 8 : 4;            // pairs of one thread
   constexpr int kLanes = D / 2 / kPairs;            // threads of one row
+  chain_begin();
   __shared__ uint64_t turn[D / 2];
   __shared__ int8_t axis[D / 2];
   if (threadIdx.x < D / 2) {
@@ -62,6 +64,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
   const int64_t row = at / kLanes;
   const int v = (int)(at % kLanes);
   if (row >= p.rows) return;
+  chain_wait();
   float cs[kPairs], sn[kPairs];
   uint32_t copied = 0;
   {
@@ -138,11 +141,12 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
 }
 
 template <int D, bool HALVES>
-void launch_rotary(const RotaryParams& p, float sign, cudaStream_t s) {
+cudaError_t launch_rotary(const RotaryParams& p, float sign, cudaStream_t s) {
   constexpr int kLanes = D / 2 / (HALVES ? 8 : 4);
   const int64_t blocks = ((int64_t)p.rows * kLanes + kRotaryThreads - 1) / kRotaryThreads;
   const int groups = (p.heads + p.heads_per_thread - 1) / p.heads_per_thread;
-  rotary_kernel<D, HALVES><<<dim3((unsigned)blocks, (unsigned)groups), kRotaryThreads, 0, s>>>(p, sign);
+  return launch_chained(rotary_kernel<D, HALVES>, dim3((unsigned)blocks, (unsigned)groups), kRotaryThreads, 0, s, 1, p,
+                        sign);
 }
 
 // The pairs' turns and axes. The last spec's are kept: working them out takes a
@@ -254,11 +258,9 @@ extern "C" int wave_rotary(wave_kv* kv, const wave_rotary_spec* spec, const int3
   p.heads_per_thread = (int)std::min<int64_t>(8, (p.heads + groups - 1) / groups);
   const float sign = spec->inverse ? -1.f : 1.f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (D == 128 && spec->layout == WAVE_ROTARY_HALVES) launch_rotary<128, true>(p, sign, s);
-  else if (D == 128) launch_rotary<128, false>(p, sign, s);
-  else if (spec->layout == WAVE_ROTARY_HALVES) launch_rotary<64, true>(p, sign, s);
-  else launch_rotary<64, false>(p, sign, s);
-  cudaError_t e = cudaGetLastError();
+  const bool halves = spec->layout == WAVE_ROTARY_HALVES;
+  const cudaError_t e = D == 128 ? (halves ? launch_rotary<128, true>(p, sign, s) : launch_rotary<128, false>(p, sign, s))
+                                 : (halves ? launch_rotary<64, true>(p, sign, s) : launch_rotary<64, false>(p, sign, s));
   if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "rotary_kernel launch: %s", cudaGetErrorString(e));
   return WAVE_OK;
 }

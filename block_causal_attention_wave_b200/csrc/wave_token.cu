@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
   auto full = [&](int s) -> uint32_t { return bars + 8u * s; };
   auto empty = [&](int s) -> uint32_t { return bars + 8u * (S + s); };
 
+  chain_begin();
   if (threadIdx.x == 0) {
     for (int t = 0; t < C::kTeams; ++t)
       for (int s = 0; s < S; ++s) {
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
     prefetch_tmap(&h.tm);
   }
   __syncthreads();
+  chain_wait();
 
   if (warp >= C::kWarps) {
     if constexpr (D == 128) regs_dec<C::kRegsFeed>();
@@ -584,8 +586,8 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
       next_mask = masks[u];
       if constexpr (FP8) {
         const int64_t page = next_word & 0x1FFFFFFu;
-        next_sk = __ldg(h.scales + (page * 2) * h.heads + head);
-        next_sv = __ldg(h.scales + (page * 2 + 1) * h.heads + head);
+        next_sk = h.scales[(page * 2) * h.heads + head];
+        next_sv = h.scales[(page * 2 + 1) * h.heads + head];
       }
     };
     fetch(u0 + team);
@@ -699,7 +701,8 @@ template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) token_join_kernel(const __grid_constant__ TokHead h,
                                                                     const int n_queries) {
   constexpr int V = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  chain_begin();
+  chain_wait();
   const int lane = threadIdx.x & 31;
   const int q_heads = h.heads * h.per_kv;
   const int at = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
@@ -747,19 +750,9 @@ int launch_token(const TokParams<CAP>& p, int device, cudaStream_t s) {
   if (D == 128 && regs < C::kRegsLaunch)
     return fail(WAVE_ERR_UNSUPPORTED, "token_attn_kernel compiled with %d registers per thread; its "
                 "register split needs %d", regs, C::kRegsLaunch);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.h.n_groups * p.h.heads * p.h.parts * p.h.cluster));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)p.h.cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.h.cluster > 1 ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, token_attn_kernel<D, FP8, QT, CAP>, p);
-  if (e != cudaSuccess) cudaGetLastError();
+  const unsigned grid = (unsigned)(p.h.n_groups * p.h.heads * p.h.parts * p.h.cluster);
+  const cudaError_t e = launch_chained(token_attn_kernel<D, FP8, QT, CAP>, dim3(grid), C::kThreads, C::kSmemBytes, s,
+                                       (unsigned)p.h.cluster, p);
   if (e != cudaSuccess) return fail(WAVE_ERR_CUDA, "token_attn_kernel launch: %s", cudaGetErrorString(e));
   return WAVE_OK;
 }
@@ -992,21 +985,10 @@ extern "C" int wave_token_attn(wave_kv* kv, const wave_node* active, int32_t n_a
     rc = launch_token_rows(kv, t.p, s);
   }
   if (rc || h.parts == 1) return rc;
-  // The second kernel's launch overlaps the first's end (its blocks wait for it).
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((int64_t)n_active * q_heads + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = D == 128 ? cudaLaunchKernelEx(&cfg, token_join_kernel<128>, h, (int)n_active)
-                           : cudaLaunchKernelEx(&cfg, token_join_kernel<64>, h, (int)n_active);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
+  const dim3 grid((unsigned)(((int64_t)n_active * q_heads + kJoinWarps - 1) / kJoinWarps));
+  const cudaError_t e = D == 128 ? launch_chained(token_join_kernel<128>, grid, 32 * kJoinWarps, 0, s, 1, h, (int)n_active)
+                                 : launch_chained(token_join_kernel<64>, grid, 32 * kJoinWarps, 0, s, 1, h, (int)n_active);
+  if (e != cudaSuccess)
     return fail(WAVE_ERR_CUDA, "token_join_kernel launch: %s", cudaGetErrorString(e));
-  }
   return WAVE_OK;
 }

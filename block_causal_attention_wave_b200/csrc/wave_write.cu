@@ -23,6 +23,7 @@
 
 #include "ptx.cuh"
 #include "wave_internal.h"
+#include "wave_wait.cuh"
 
 namespace wavei {
 namespace {
@@ -93,7 +94,7 @@ __device__ __forceinline__ WriteTile write_tile(const P& p, int tile) {
 
 template <class P>
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_constant__ P p) {
-  if (blockIdx.x >= p.n_tiles) return;
+  chain_begin();
   const WriteTile t = write_tile(p, blockIdx.x);
   const int vec = 1 << p.log2_vec;
   const uint16_t* src = (t.kv ? p.v : p.k) + (t.row - t.r0) * (t.kv ? p.ldv : p.ldk) +
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
                ((int64_t)t.kv * p.heads + t.head) * WAVE_PAGE_TOKENS * vec;
   const int from = t.r0 * vec;
   const int to = (t.held == 0 ? WAVE_PAGE_TOKENS : t.r1) * vec;
+  chain_wait();
   uint4 val[kWritePer];
 #pragma unroll
   for (int u = 0; u < kWritePer; ++u) {
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
     const int r = i >> p.log2_vec;
     val[u] = make_uint4(0, 0, 0, 0);
     if (i < to && r < t.r1)
-      val[u] = __ldg(reinterpret_cast<const uint4*>(src + r * ld) + (i & (vec - 1)));
+      val[u] = *(reinterpret_cast<const uint4*>(src + r * ld) + (i & (vec - 1)));
   }
 #pragma unroll
   for (int u = 0; u < kWritePer; ++u) {
@@ -171,7 +173,7 @@ template <int THREADS, class P>
 __global__ void __launch_bounds__(THREADS) kv_write_fp8_kernel(const __grid_constant__ P p) {
   constexpr int kPer = WAVE_PAGE_TOKENS * 16 / THREADS;  // vectors per thread, d = 128
   __shared__ float warp_max[THREADS / 32];
-  if (blockIdx.x >= p.n_tiles) return;
+  chain_begin();
   const WriteTile t = write_tile(p, blockIdx.x);
   const int vec = 1 << p.log2_vec;  // 8-value vectors per row
   const uint16_t* src = (t.kv ? p.v : p.k) + (t.row - t.r0) * (t.kv ? p.ldv : p.ldk) +
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(THREADS) kv_write_fp8_kernel(const __grid_cons
   uint2* dst = reinterpret_cast<uint2*>(p.data + t.page * p.page_bytes) +
                ((int64_t)t.kv * p.heads + t.head) * WAVE_PAGE_TOKENS * vec;
   float* scale = p.scales + (t.page * 2 + t.kv) * p.heads + t.head;
+  chain_wait();
   const float old = *scale;
   uint4 val[kPer];  // new rows: 8 bf16 values; kept rows: 8 codes in x, y
   float amax = 0.f;
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(THREADS) kv_write_fp8_kernel(const __grid_cons
     const int r = i >> p.log2_vec;
     val[u] = make_uint4(0, 0, 0, 0);
     if (r >= t.r0 && r < t.r1) {
-      val[u] = __ldg(reinterpret_cast<const uint4*>(src + r * ld) + (i & (vec - 1)));
+      val[u] = *(reinterpret_cast<const uint4*>(src + r * ld) + (i & (vec - 1)));
     } else if (r < t.held) {
       const uint2 c = dst[i];
       val[u].x = c.x;
@@ -254,13 +257,11 @@ __global__ void __launch_bounds__(THREADS) kv_write_fp8_kernel(const __grid_cons
 }
 
 template <class P>
-void launch_write(bool fp8, const P& p, int sms, cudaStream_t s) {
-  if (fp8 && p.n_tiles <= 4 * sms)
-    kv_write_fp8_kernel<512, P><<<(unsigned)p.n_tiles, 512, 0, s>>>(p);
-  else if (fp8)
-    kv_write_fp8_kernel<256, P><<<(unsigned)p.n_tiles, 256, 0, s>>>(p);
-  else
-    kv_write_kernel<P><<<(unsigned)p.n_tiles, kWriteThreads, 0, s>>>(p);
+cudaError_t launch_write(bool fp8, const P& p, int sms, cudaStream_t s) {
+  const dim3 grid((unsigned)p.n_tiles);
+  if (!fp8) return launch_chained(kv_write_kernel<P>, grid, kWriteThreads, 0, s, 1, p);
+  return p.n_tiles <= 4 * sms ? launch_chained(kv_write_fp8_kernel<512, P>, grid, 512, 0, s, 1, p)
+                              : launch_chained(kv_write_fp8_kernel<256, P>, grid, 256, 0, s, 1, p);
 }
 
 }  // namespace
@@ -331,16 +332,16 @@ extern "C" int wave_kv_write_tokens(wave_kv* kv, int32_t n_entries, const wave_n
   p.n_entries = n;
   p.n_tiles = (int32_t)tiles;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
   if (n <= 8 && pages <= 64) {
     WriteParamsSmall q;
     std::memcpy(&q, &p, offsetof(WriteParamsSmall, e));
     std::memcpy(q.e, p.e, n * sizeof(WriteEntry));
     std::memcpy(q.pages, p.pages, pages * sizeof(int32_t));
-    launch_write(kv->fp8, q, kv->num_sms, s);
+    e = launch_write(kv->fp8, q, kv->num_sms, s);
   } else {
-    launch_write(kv->fp8, p, kv->num_sms, s);
+    e = launch_write(kv->fp8, p, kv->num_sms, s);
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess)
     return fail(WAVE_ERR_CUDA, "kv_write_kernel launch: %s", cudaGetErrorString(e));
   for (int i = 0; i < n; ++i)
