@@ -24,14 +24,12 @@
 //     in the workspace for a second kernel.
 //   - Warps are two or three teams that take every other unit; a warp takes 32 of
 //     the page's 128 keys, for all rows, with its own running maximum, sum
-//     and O: no exchange between warps until the segment ends.
+//     and O: no exchange between warps until the CTA's items end.
 //   - A further warp per team feeds it, K and V tiles by TMA through a ring of the
 //     team's own (192 KB in flight per SM in all). A ring that the teams shared
 //     would need every warp at every slot: a parity wait tells apart only the
 //     phase after the last one its waiter saw, so a team that skipped the other
-//     team's fill of a slot could take it for its own. S = Q K^T and O += P V are m16n8k16 MMAs on fragments read
-//     from shared memory; one token fills one of 16 rows, but at a byte a cycle
-//     a thread the tensor pipe idles either way, and 16 rows cost what one costs.
+//     team's fill of a slot could take it for its own.
 //   - Both products are m16n8k16 MMAs with the cache as the operand of sixteen rows:
 //     S^T = K Q^T (16 keys x 8 query rows) and O^T += V^T P^T (16 d x 8 query
 //     rows), QT = 1 or 2 tiles of query rows. With the queries as the sixteen rows
@@ -601,14 +599,15 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
       if (!dead) dead = !__all_sync(0xffffffffu, wait_within(full(ks), kp, ctl, 0x402));
       if (dead) continue;
       // The common unit, of which every row sees every token, has code of its own:
-      // with the selections for the others in line (predicated by the compiler)
-      // a unit took 919 instructions a warp instead of 473 (queries as the sixteen rows).
+      // with the others' selections in line (predicated by the compiler) a unit
+      // took twice the instructions (919 a warp, then 473, with the queries still
+      // as the sixteen rows).
       const bool whole = seen == kPageTokens && (mask & all_rows) == all_rows;
       if (whole) dead = !unit(std::true_type{}, ks, vs, vp, seen, mask, sk, sv);
       else dead = !unit(std::false_type{}, ks, vs, vp, seen, mask, sk, sv);
     }
 
-    // ---- join the eight warps: O of each, scaled to the CTA's maximum, goes into
+    // ---- join the warps: O of each, scaled to the CTA's maximum, goes into
     // the ring, whose tiles all warps are done with at the first barrier.
     float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
     float* red = reinterpret_cast<float*>(smem);
@@ -778,16 +777,18 @@ void cut_lists(TokHead& h, int32_t longest) {
   h.cluster = 1;
   double best = 1e30;
   for (int s = 1; s <= 8 && s <= std::max(1, longest); ++s) {
-    // Waves of clusters; an item takes 0.46 of its time at a 148th of HBM's rate
-    // when an SM draws all it can, more once the SMs share HBM; a wave costs
-    // about two items to start and end.
+    // Waves of clusters; in units of an item's time at a 148th of HBM's rate, an
+    // item takes 0.6 when an SM draws all it can, more once the SMs share HBM, and
+    // a wave two to start and end.
     const double waves = (double)((lists + kHeld[s] - 1) / kHeld[s]);
     const double active = (double)std::min<int64_t>(lists, kHeld[s]) * s;
     const double t = waves * ((longest + s - 1) / s * std::max(0.6, active / 148.0) + 2.0);
     if (t < best) best = t, h.cluster = s;
   }
-  // Few long lists: several clusters each, while every CTA keeps eight items (the
-  // second kernel costs about as much as two).
+  // Fewer than 8 long lists: several clusters each, while every CTA keeps eight
+  // items. The second kernel takes 6 us: one head over 41 chunks of 4680 tokens
+  // takes 28 us in 15 clusters, where one would draw 0.7 TB/s for 130; 8 lists of
+  // 290 items gain nothing (20 us and 20).
   if (lists * 8 < 64 && longest >= 128) {
     h.cluster = 8;
     h.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(kHeld[8] / lists, longest / 64));

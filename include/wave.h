@@ -423,11 +423,12 @@ int wave_round_attn_split_workspace(wave_kv* kv, const wave_node* active, int32_
  * of 8, >= q_heads * d; 16-byte aligned pointers (lse: 4). O overlaps nothing.
  * bf16 and FP8 pools: an FP8 page is read in place, its values code * s in
  * float32 without the rounding to bf16 of wave_round_attn_split.
- * The key lists are cut over the GPU's SMs in pages and joined by a second
- * launch; a page that several queries read is read once for up to 16 / (q_heads
- * / H) of them that follow one another in the list. Sums run in a fixed order:
- * equal calls give equal bytes. A query's last bits may depend on the other
- * queries of the call, through where its list is cut.
+ * The key lists are cut over the GPU's SMs in pages and joined in the same
+ * launch (a few long lists in a second one, through the workspace); a page that
+ * several queries read is read once for up to 16 / (q_heads / H) of them that
+ * follow one another in the list. Sums run in a fixed order: equal calls give
+ * equal bytes. A query's last bits may depend on the other queries of the call,
+ * through where its list is cut.
  * workspace: device buffer, 256-byte aligned, of at least
  * wave_token_attn_workspace bytes for the same arguments (NULL if that is 0);
  * scratch, not shared by calls whose kernels may overlap. Limits: n_active <=

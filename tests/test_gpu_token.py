@@ -703,6 +703,37 @@ def test_linear_timeout_is_reported(cuda_lib, M, K, N):
     assert (y == K * 2.0 ** -10).all()   # 4, 8.75 or 1.5: exact in bf16
 
 
+@FORMATS
+def test_pages_past_four_gigabytes(cuda_lib, fp8):
+    """Entries at the end of a pool of 10 GB: page offsets pass 32 bits."""
+    import torch
+    H, d, T = 24, 128, 300
+    fmt = cuda_lib.KV_FP8_E4M3 if fp8 else cuda_lib.KV_BF16
+    per = cuda_lib.KVCache.page_bytes(H, d, fmt)
+    pages = 10 * 2 ** 30 // per
+    w = _World(cuda_lib, H, d, T, 1, fp8=fp8, pages=1)
+    w.kv = kv = _cache(cuda_lib, H, d, T, 1, pages=pages, fp8=fp8)
+    filler = 0
+    while kv.free_pages() >= 12:        # three pages each; host only, nothing is written
+        kv.alloc(100 + filler, 1)
+        filler += 1
+    for c in range(2):
+        w.add(c, 0)
+    kv.alloc(2, 1)
+    assert min(kv.entry_pages(2, 1)) * per > 9 * 2 ** 30
+    k, v = (_bf(w.rng, T, H, d) for _ in range(2))
+    kv.write_tokens([(2, 1)], [0], _dev(k[:200]), _dev(v[:200]), [200])
+    kv.write_tokens([(2, 1)], [200], _dev(k[200:]), _dev(v[200:]), [100])
+    if fp8:
+        ents = [otok.Fp8Entry(T, H, d) for _ in range(2)]
+        for e, x in zip(ents, (k, v)):
+            e.write(0, x[:200])
+            e.write(200, x[200:])
+        k, v = (e.values(T) for e in ents)
+    w.entries[2, 1] = (k, v)
+    w.check([(2, 1), (2, 1)], own=[300, 129], what="far pages")
+
+
 def test_token_attn_two_streams(cuda_lib):
     """Calls on two streams at once, a workspace each, and one on a third stream
     with other sizes: the results of calls alone."""
