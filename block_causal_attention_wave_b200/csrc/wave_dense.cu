@@ -20,27 +20,26 @@ int launch_tokens(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
 }
 
 // More rows: the cheapest form by its cost in us: a start and end, more where the
-// parts of K are joined, and what a 64-wide slice of K takes, which is the issuing
-// thread's time per slice more than the tile's size (and, for pairs in several
-// waves, the clock under load). Against a sweep over M = 40 .. 4680 and K x N =
-// 1536 x 1536 .. 4096 x 4096 the choice is the best form or within 10 % of it. Both
-// sides: 984 x 8960 x 1536: 192-column pairs with K in two 32.6, 256-column 34.6, in
-// one 50.8, 128-column tiles 48.2; 256 x 1536 x 1536: 64-column tiles with K in two
-// 10.7, 128-column in four 11.6, pairs 15.5; 512 x 1536 x 4608: 128-column tiles
-// 14.4, pairs 15.7, 64-column tiles 23.3; 2000 x 1536 x 8960: 256-column pairs 47.5,
-// 192-column 59.5, 128-column tiles 100. kHeld[c]: clusters of c CTAs that a B200
-// holds at a time (occupancy query).
+// parts of K are joined, and what a 128-wide slice of K takes (for pairs in several
+// waves, at the clock under load). Against a sweep over M = 40 .. 4680 and K x N =
+// 1536 x 1536 .. 4096 x 4096 the choice is the best form or within a few percent
+// of it. Both sides: 984 x 8960 x 1536: 192-column pairs with K in two 29.9,
+// 256-column 34.5, 128-column tiles 38.6; 256 x 1536 x 1536: 64-column tiles with K
+// in two 8.4, 128-column in four 9.6, pairs 13; 512 x 1536 x 4608: 128-column tiles
+// 11.2, pairs 13.6; 2000 x 1536 x 8960: 256-column pairs 44, 192-column 50,
+// 128-column tiles 83. kHeld[c]: clusters of c CTAs that a B200 holds at a time
+// (occupancy query).
 int launch_rows(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
   constexpr int kHeld[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
   struct Form {
-    int rows, cols, ctas, most;   // tile, CTAs that share one, most parts of K
-    double start, slice, loaded;  // `loaded`: a slice in more than one wave
+    int rows, cols, ctas, most;         // tile, CTAs that share one, most parts of K
+    double start, join, slice, loaded;  // `loaded`: a slice in more than one wave
   };
-  constexpr Form kForms[4] = {{128, 64, 1, 8, 6.5, 0.28, 0.28},
-                              {128, 128, 1, 8, 8.0, 0.30, 0.30},
-                              {256, 192, 2, 4, 10.5, 0.25, 0.31},
-                              {256, 256, 2, 4, 11.0, 0.32, 0.35}};
-  const int64_t slices = (a.K + 63) / 64;
+  constexpr Form kForms[4] = {{128, 64, 1, 8, 4.5, 1.5, 0.40, 0.40},
+                              {128, 128, 1, 8, 5.3, 3.5, 0.49, 0.49},
+                              {256, 192, 2, 4, 6.7, 3.5, 0.55, 0.62},
+                              {256, 256, 2, 4, 8.2, 3.5, 0.60, 0.72}};
+  const int64_t slices = (a.K + 127) / 128;
   double best = 1e30;
   int form = 3, parts = 1;
   for (int f = 0; f < 4; ++f)
@@ -51,7 +50,7 @@ int launch_rows(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
       const double waves = (double)((tiles + held - 1) / held);
       // Pairs that do not share K are persistent: their tiles follow without a gap.
       const bool persistent = x.ctas == 2 && n == 1;
-      const double t = (persistent ? 1.0 : waves) * (x.start + (n > 1 ? 2.5 : 0.0)) +
+      const double t = (persistent ? 1.0 : waves) * (x.start + (n > 1 ? x.join : 0.0)) +
                        waves * (double)((slices + n - 1) / n) * (waves > 1 ? x.loaded : x.slice);
       if (t < best) best = t, form = f, parts = n;
     }

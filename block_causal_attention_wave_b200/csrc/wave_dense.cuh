@@ -200,10 +200,10 @@ int encode_kmajor(CUtensorMap* map, const void* base, int64_t rows, int64_t k, u
 // or (ft = 1, at most 8 rows) 16.
 int token_rows_launch(const DenseArgs& a, int ft, int warps, cudaStream_t s);
 // wave_few.cu. Tiles of 128 rows x nf features (64 or 128), K cut over clusters of
-// `splits` CTAs (1 .. 8, at most the 64-wide slices of K).
+// `splits` CTAs (1 .. 8, at most the 128-wide slices of K).
 int split_rows_launch(const struct ::wave_kv* kv, const DenseArgs& a, int nf, int splits, cudaStream_t s);
 // wave_pair.cu. Tiles of 256 rows x nt columns (192 or 256) on pairs of SMs; splits > 1
-// (2 .. 4, at most the 64-wide slices of K): K cut over the pairs of a cluster.
+// (2 .. 4, at most the 128-wide slices of K): K cut over the pairs of a cluster.
 int pair_rows_launch(const struct ::wave_kv* kv, const DenseArgs& a, int nt, int splits, cudaStream_t s);
 
 }  // namespace wavei

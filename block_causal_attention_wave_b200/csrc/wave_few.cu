@@ -175,7 +175,8 @@ constexpr int kSplitThreads = 192;
 template <int NF>
 struct SplitCfg {
   static constexpr int kATile = 128 * 128;  // 128 rows x 64 bf16
-  static constexpr int kStage = kATile + NF * 128;
+  static constexpr int kWTile = NF * 128;
+  static constexpr int kStage = 2 * (kATile + kWTile);  // two panels of 64 of each: K = 128
   static constexpr int kStages = 196608 / kStage;
   static constexpr int kBarOff = kStages * kStage;
   static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kDrain = kAccFull + 1,
@@ -273,15 +274,19 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
   if (warp == 0) {
     if (lane == 0) {
       // Rows past box_rows are left as they are: they only reach unused rows.
-      const uint32_t bytes = NF * 128 + p.box_rows * 128;
+      const uint32_t bytes = 2 * (NF * 128 + p.box_rows * 128);
       int n = 0;
       int s = 0;
       uint32_t ph = 1;
       for (int k = k0; k < k1; ++k, ++n) {
         if (n >= S && !wait_within(bar(C::kEmpty + s), ph, ctl, 0x501)) break;
         mbar_arrive_expect_tx(bar(C::kFull + s), bytes);
-        tma_load_2d(sb + s * C::kStage + C::kATile, &p.tm_w, k * 64, ft * NF, bar(C::kFull + s));
-        tma_load_2d(sb + s * C::kStage, &p.tm_a, k * 64, mt * 128, bar(C::kFull + s));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t a = sb + s * C::kStage + j * C::kATile, w = sb + s * C::kStage + 2 * C::kATile + j * C::kWTile;
+          tma_load_2d(w, &p.tm_w, k * 128 + j * 64, ft * NF, bar(C::kFull + s));
+          tma_load_2d(a, &p.tm_a, k * 128 + j * 64, mt * 128, bar(C::kFull + s));
+        }
         if (++s == S) s = 0, ph ^= 1;
       }
       // Copies still in flight land before the ring is reused or the CTA exits.
@@ -300,7 +305,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __gr
           break;
         }
         const uint32_t lo = lo0 + (uint32_t)s * (C::kStage >> 4);
-        mma_slice(tmem, lo, lo + (C::kATile >> 4), hi, C::kIdesc, n != 0);
+        mma_slice(tmem, lo, lo + (2 * C::kATile >> 4), hi, C::kIdesc, n != 0);
+        mma_slice(tmem, lo + (C::kATile >> 4), lo + ((2 * C::kATile + C::kWTile) >> 4), hi, C::kIdesc, 1);
         tc_commit(bar(C::kEmpty + s));
         if (++s == S) s = 0, ph ^= 1;
       }
@@ -406,7 +412,7 @@ int split_rows_launch(const wave_kv* kv, const DenseArgs& a, int nf, int splits,
   if (int rc = encode_kmajor(&p.tm_a, a.A, a.M, a.K, (uint32_t)p.box_rows, "A", a.lda)) return rc;
   p.status = static_cast<int32_t*>(kv->cfg.pool);
   p.wait_ns = wait_limit_ns(kv);
-  p.k_slices = (a.K + 63) / 64;
+  p.k_slices = (a.K + 127) / 128;  // the tensor maps fill K's tail with zeros
   p.n_ftiles = (a.N + nf - 1) / nf;
   p.splits = splits;
   p.M = a.M;

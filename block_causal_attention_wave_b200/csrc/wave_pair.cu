@@ -10,7 +10,7 @@
 // own 128 rows of A and half of W's rows, 32 KB per 512 cycles.
 //
 // How: 74 persistent pairs walk the tiles row-tile-major (A comes from HBM once,
-// the weights stay in L2). Per CTA: warp 0 lane 0 feeds a 6- or 7-stage ring by TMA,
+// the weights stay in L2). Per CTA: warp 0 lane 0 feeds a 3-stage ring (K = 128 each) by TMA,
 // both CTAs' bytes counted on the even CTA's barrier; warp 1 lane 0 of the even
 // CTA issues the MMAs of both into one of two 256-column TMEM accumulators;
 // warps 2..9 are the epilogue, two warps per 32 rows, while the other accumulator
@@ -43,7 +43,7 @@ template <int NT>
 struct PairCfg {
   static constexpr int kATile = 128 * 128;      // 128 rows x 64 bf16
   static constexpr int kWTile = NT / 2 * 128;   // half of the columns' rows of W
-  static constexpr int kStage = kATile + kWTile;
+  static constexpr int kStage = 2 * (kATile + kWTile);   // two panels of 64 of each: K = 128
   static constexpr int kStages = 204800 / kStage;
   static constexpr int kBarOff = kStages * kStage;
   static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2,
@@ -182,8 +182,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
           }
           const uint32_t a = sb + s * C::kStage;
           if (half == 0) mbar_arrive_expect_tx(bar(C::kFull + s), 2 * C::kStage);
-          tma_load_pair(a, &p.tm_a, k * 64, mt * 256 + half * 128, full0 + 8u * s);
-          tma_load_pair(a + C::kATile, &p.tm_w, k * 64, nt * NT + half * (NT / 2), full0 + 8u * s);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            tma_load_pair(a + j * C::kATile, &p.tm_a, k * 128 + j * 64, mt * 256 + half * 128, full0 + 8u * s);
+            tma_load_pair(a + 2 * C::kATile + j * C::kWTile, &p.tm_w, k * 128 + j * 64, nt * NT + half * (NT / 2),
+                          full0 + 8u * s);
+          }
           if (++s == S) s = 0, ph ^= 1;
         }
       }
@@ -199,9 +203,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
     }
   } else if (warp == 1) {
     if (lane == 0 && half == 0) {
-      // This thread's instructions per slice are what bounds the loop (410 of 604
-      // cycles, with a division, a fence and a 64-bit descriptor per MMA): the
-      // ring's position is kept, not computed, and a slice's MMAs are one block.
+      // This thread's own time bounds the loop unless it is short against the MMAs it
+      // issues, and more so while the epilogue's warps take issue slots: 604 cycles
+      // per 64 of K (512 of the tensor pipe's) with a division, a fence and a 64-bit
+      // descriptor per MMA; 563, and 660 under a GELU epilogue, with the ring's
+      // position kept and four MMAs in one block; 524 and 535 with 128 of K per
+      // wait and commit.
       const uint64_t desc = desc_k(sb);
       const uint32_t hi = (uint32_t)(desc >> 32), lo0 = (uint32_t)desc;
       int s = 0, i = 0;
@@ -218,7 +225,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
             break;
           }
           const uint32_t lo = lo0 + (uint32_t)s * (C::kStage >> 4);
-          mma_pair_slice(tmem + 256 * acc, lo, lo + (C::kATile >> 4), hi, C::kIdesc, accumulate);
+          mma_pair_slice(tmem + 256 * acc, lo, lo + (2 * C::kATile >> 4), hi, C::kIdesc, accumulate);
+          mma_pair_slice(tmem + 256 * acc, lo + (C::kATile >> 4), lo + ((2 * C::kATile + C::kWTile) >> 4), hi, C::kIdesc, 1);
           accumulate = 1;
           commit_pair(bar(C::kEmpty + s), both);
           if (++s == S) s = 0, ph ^= 1;
@@ -335,7 +343,7 @@ int pair_rows_launch(const wave_kv* kv, const DenseArgs& a, int nt, int splits, 
   if (int rc = encode_kmajor(&p.tm_w, a.W, a.N, a.K, (uint32_t)nt / 2, "W")) return rc;
   p.status = static_cast<int32_t*>(kv->cfg.pool);
   p.wait_ns = wait_limit_ns(kv);
-  p.k_slices = (a.K + 63) / 64;
+  p.k_slices = (a.K + 127) / 128;  // the tensor maps fill K's tail with zeros
   p.n_ntiles = (a.N + nt - 1) / nt;
   const int64_t tiles = ((int64_t)a.M + 255) / 256 * p.n_ntiles;
   if (tiles >= (1LL << 28)) return fail(WAVE_ERR_ARG, "M x N too large");
