@@ -89,6 +89,7 @@ extern "C" int wave_linear_bias(wave_kv* kv, const void* A, int64_t lda, int32_t
       (R && (ldr < N || ldr % 8 || ldr >= most)))
     return fail(WAVE_ERR_ARG, "row strides must be multiples of 8 and cover the row; got lda %lld, "
                 "ldr %lld, ldy %lld", (long long)lda, (long long)ldr, (long long)ldy);
+  if (Y && (Y == A || Y == W || Y == bias)) return fail(WAVE_ERR_ARG, "Y may overlap nothing but R");
   if (R && R == Y && ldr != ldy) return fail(WAVE_ERR_ARG, "Y = R needs ldy = ldr");
   if (M == 0) return WAVE_OK;
   if (!A || !W || !Y || !aligned16(A) || !aligned16(W) || !aligned16(Y) || (R && !aligned16(R)) ||

@@ -47,7 +47,7 @@ __device__ __forceinline__ float activate(float x) {
     e = fmaf(e, t, -0.284496736f);
     e = fmaf(e, t, 0.254829592f);
     const float h = 0.5f * x * (e * t * wptx::ex2_approx(-1.442695041f * z * z));
-    return x < 0.f ? h : x - h;
+    return x < 0.f ? h : x < 16.f ? x - h : x;  // from 16 on h is less than half a step; at infinity, NaN
   }
   return x;
 }

@@ -683,11 +683,11 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
     } else {
       const int64_t query = grp.q0 + row / h.per_kv;
       const int qhead = head * h.per_kv + row % h.per_kv;
-      const float v = top == -INFINITY ? 0.f : sum / den;
+      const float v = den == 0.f ? 0.f : sum / den;  // 0: no token seen; NaN scores have a NaN sum
       h.o[query * h.ldo + (int64_t)qhead * D + d] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFF);
       if (h.lse && d == 0)
         h.lse[query * (h.heads * h.per_kv) + qhead] =
-            top == -INFINITY ? -INFINITY : (top + log2f(den)) * 0.6931471805599453f;
+            den == 0.f ? -INFINITY : (top + log2f(den)) * 0.6931471805599453f;
     }
   }
   __syncwarp();
@@ -724,14 +724,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) token_join_kernel(const __gri
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] += e * h.part_o[slot * D + lane * V + i];
   }
-  const float inv = mx == -INFINITY ? 0.f : 1.f / den;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
   uint16_t* dst = h.o + query * h.ldo + (int64_t)qhead * D + lane * V;
 #pragma unroll
   for (int i = 0; i < V; i += 2)
     *reinterpret_cast<uint32_t*>(dst + i) =
-        mx == -INFINITY ? 0u : pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+        den == 0.f ? 0u : pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
   if (h.lse && lane == 0)
-    h.lse[at] = mx == -INFINITY ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
+    h.lse[at] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
 }
 
 template <int D, bool FP8, int QT, int CAP>

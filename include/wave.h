@@ -338,7 +338,11 @@ int wave_kv_free_pages(const wave_kv* kv, int32_t* n);
  * elements, multiples of 8, >= H * d; 16-byte aligned pointers. Limits:
  * n_entries <= WAVE_MAX_APPEND_ENTRIES, touched pages <= WAVE_MAX_APPEND_PAGES
  * in all (CAPACITY). Errors: ARG, MISSING_KV (an entry without pages), CAPACITY,
- * CUDA; on any error nothing is written or counted. */
+ * CUDA; on any error nothing is written or counted.
+ * Captured into a graph, a write counts when it is captured and each replay
+ * writes as it would have then: what it takes for unwritten becomes zero (bf16:
+ * of a page's first write) or keeps its code while the scale grows (FP8). So
+ * replay it only while no token behind its own has been written. */
 int wave_kv_write_tokens(wave_kv* kv, int32_t n_entries, const wave_node* entries,
                          const int32_t* first, const int32_t* ntokens, const void* K, int64_t ldk,
                          const void* V, int64_t ldv, void* stream);
@@ -415,7 +419,8 @@ int wave_round_attn_split_workspace(wave_kv* kv, const wave_node* active, int32_
  * exist. The tokens counted must have been written (on this stream or before
  * it). A node may be listed several times (several tokens of one entry, each
  * with its own count). q_heads: a multiple of H, at most 16 H. A query that sees
- * no token gets O = 0 and lse = -inf.
+ * no token (or whose scores are all -inf) gets O = 0 and lse = -inf; NaN in what
+ * it sees reaches its result.
  * Q: device bf16, n_active rows of [q_heads][d], row stride ldq; O likewise with
  * ldo, written; lse: device float32 [n_active][q_heads], written, or NULL: the
  * natural logarithm of the sum of exp(score) over the tokens seen, from which

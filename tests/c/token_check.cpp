@@ -73,33 +73,37 @@ int main(int argc, char** argv) {
   wave_kv* kv = handle(2, 64, 256, 2, 0, 100, 40, true);
 
   // ---- dense layer
+  const uint16_t *a = p + 1024, *w = p + 2048;
   auto lin = [&](const void* A, int64_t lda, int M, int K, const void* W, int N, const void* b, const void* R,
                  int64_t ldr, int act, void* Y, int64_t ldy) {
     return wave_linear_bias(kv, A, lda, M, K, W, N, b, R, ldr, act, Y, ldy, nullptr);
   };
-  expect(lin(p, 64, 3, 64, p, 64, p, p, 64, 3, p, 64), stop, "linear: good arguments reach the device check");
+  expect(lin(a, 64, 3, 64, w, 64, a, p, 64, 3, p, 64), stop, "linear: good arguments reach the device check");
   expect(lin(nullptr, 64, 0, 64, nullptr, 64, nullptr, nullptr, 0, 0, nullptr, 64), WAVE_OK, "linear: no rows");
-  expect(lin(p, 64, -1, 64, p, 64, p, p, 64, 0, p, 64), bad, "linear: M < 0");
-  expect(lin(p, 64, (1 << 30) + 1, 64, p, 8, p, p, 64, 0, p, 64), bad, "linear: M > 2^30");
-  expect(lin(p, 64, 3, 60, p, 64, p, p, 64, 0, p, 64), bad, "linear: K % 8");
-  expect(lin(p, 64, 3, 64, p, 60, p, p, 64, 0, p, 64), bad, "linear: N % 8");
-  expect(lin(p, 64, 3, 0, p, 64, p, p, 64, 0, p, 64), bad, "linear: K = 0");
-  expect(lin(p, 64, 3, 64, p, 0, p, p, 64, 0, p, 64), bad, "linear: N = 0");
-  expect(lin(p, 65544, 3, 65544, p, 64, p, p, 64, 0, p, 64), bad, "linear: K > 65536");
-  expect(lin(p, 56, 3, 64, p, 64, p, p, 64, 0, p, 64), bad, "linear: lda < K");
-  expect(lin(p, 68, 3, 64, p, 64, p, p, 64, 0, p, 64), bad, "linear: lda % 8");
-  expect(lin(p, 1LL << 39, 3, 64, p, 64, p, p, 64, 0, p, 64), bad, "linear: lda past the tensor map");
-  expect(lin(p, 64, 3, 64, p, 64, p, p, 56, 0, p, 64), bad, "linear: ldr < N");
-  expect(lin(p, 64, 3, 64, p, 64, p, p, 64, 0, p, 56), bad, "linear: ldy < N");
-  expect(lin(p, 64, 3, 64, p, 64, p, p, 72, 0, p, 64), bad, "linear: in place with other strides");
-  expect(lin(p, 64, 3, 64, p, 64, p, p, 64, 4, p, 64), bad, "linear: activation");
-  expect(lin(p, 64, 3, 64, p, 64, p, p, 64, -1, p, 64), bad, "linear: activation < 0");
-  expect(lin(odd, 64, 3, 64, p, 64, p, p, 64, 0, p, 64), bad, "linear: A misaligned");
-  expect(lin(p, 64, 3, 64, odd, 64, p, p, 64, 0, p, 64), bad, "linear: W misaligned");
-  expect(lin(p, 64, 3, 64, p, 64, odd, p, 64, 0, p, 64), bad, "linear: bias misaligned");
-  expect(lin(p, 64, 3, 64, p, 64, p, odd, 64, 0, p, 64), bad, "linear: R misaligned");
-  expect(lin(p, 64, 3, 64, p, 64, p, p, 64, 0, odd, 64), bad, "linear: Y misaligned");
-  expect(lin(p, 64, 3, 64, p, 64, p, p, 64, 0, nullptr, 64), bad, "linear: no Y");
+  expect(lin(a, 64, -1, 64, w, 64, a, p, 64, 0, p, 64), bad, "linear: M < 0");
+  expect(lin(a, 64, (1 << 30) + 1, 64, w, 8, a, p, 64, 0, p, 64), bad, "linear: M > 2^30");
+  expect(lin(a, 64, 3, 60, w, 64, a, p, 64, 0, p, 64), bad, "linear: K % 8");
+  expect(lin(a, 64, 3, 64, w, 60, a, p, 64, 0, p, 64), bad, "linear: N % 8");
+  expect(lin(a, 64, 3, 0, w, 64, a, p, 64, 0, p, 64), bad, "linear: K = 0");
+  expect(lin(a, 64, 3, 64, w, 0, a, p, 64, 0, p, 64), bad, "linear: N = 0");
+  expect(lin(a, 65544, 3, 65544, w, 64, a, p, 64, 0, p, 64), bad, "linear: K > 65536");
+  expect(lin(a, 56, 3, 64, w, 64, a, p, 64, 0, p, 64), bad, "linear: lda < K");
+  expect(lin(a, 68, 3, 64, w, 64, a, p, 64, 0, p, 64), bad, "linear: lda % 8");
+  expect(lin(a, 1LL << 39, 3, 64, w, 64, a, p, 64, 0, p, 64), bad, "linear: lda past the tensor map");
+  expect(lin(a, 64, 3, 64, w, 64, a, p, 56, 0, p, 64), bad, "linear: ldr < N");
+  expect(lin(a, 64, 3, 64, w, 64, a, p, 64, 0, p, 56), bad, "linear: ldy < N");
+  expect(lin(a, 64, 3, 64, w, 64, a, p, 72, 0, p, 64), bad, "linear: in place with other strides");
+  expect(lin(a, 64, 3, 64, w, 64, a, p, 64, 4, p, 64), bad, "linear: activation");
+  expect(lin(a, 64, 3, 64, w, 64, a, p, 64, -1, p, 64), bad, "linear: activation < 0");
+  expect(lin(odd, 64, 3, 64, w, 64, a, p, 64, 0, p, 64), bad, "linear: A misaligned");
+  expect(lin(a, 64, 3, 64, odd, 64, a, p, 64, 0, p, 64), bad, "linear: W misaligned");
+  expect(lin(a, 64, 3, 64, w, 64, odd, p, 64, 0, p, 64), bad, "linear: bias misaligned");
+  expect(lin(a, 64, 3, 64, w, 64, a, odd, 64, 0, p, 64), bad, "linear: R misaligned");
+  expect(lin(a, 64, 3, 64, w, 64, a, p, 64, 0, odd, 64), bad, "linear: Y misaligned");
+  expect(lin(a, 64, 3, 64, w, 64, a, p, 64, 0, nullptr, 64), bad, "linear: no Y");
+  expect(lin(p, 64, 3, 64, w, 64, a, nullptr, 0, 0, p, 64), bad, "linear: Y is A");
+  expect(lin(a, 64, 3, 64, p, 64, a, nullptr, 0, 0, p, 64), bad, "linear: Y is W");
+  expect(lin(a, 64, 3, 64, w, 64, p, nullptr, 0, 0, p, 64), bad, "linear: Y is bias");
   expect(wave_linear(kv, p, 3, 64, p, 256, nullptr, WAVE_ACT_SILU, p, nullptr) < 0, 1, "wave_linear refuses SiLU");
 
   // ---- rotary

@@ -152,6 +152,23 @@ def test_linear_extremes(cuda_lib):
             assert (y[2] == 300).all() and (y[3] == (-300.0 if act == "none" else 0.0)).all(), act
 
 
+@pytest.mark.parametrize("M", [3, 140, 2400])
+@pytest.mark.parametrize("act", ["none", "gelu_tanh", "gelu_erf", "silu"])
+def test_linear_infinities(cuda_lib, act, M):
+    """Every activation's limit: +inf stays; -inf is NaN (-inf times zero) but for none."""
+    import torch
+    kv = _cache(cuda_lib)
+    a, w = np.full((M, 8), 1.0), np.full((1536 if M > 200 else 16, 8), 1.0)
+    a[0] = a[M - 1] = np.inf
+    a[1] = -np.inf
+    Y = torch.empty(M, w.shape[0], dtype=torch.bfloat16, device="cuda")
+    kv.linear_bias(_dev(a), _dev(w), Y, act=act)
+    y = torch_to_f64(Y)
+    assert np.isposinf(y[[0, M - 1]]).all()
+    assert np.isneginf(y[1]).all() if act == "none" else np.isnan(y[1]).all()
+    assert np.isfinite(y[2:M - 1]).all()
+
+
 # ------------------------------------------------------------------ rotary
 def _rotary_tol(x, ref):
     size = np.abs(x).max(-1, keepdims=True) * 2
@@ -531,6 +548,32 @@ def test_token_attn_garbage_behind_the_mask(cuda_lib, fp8):
 
 
 @FORMATS
+@pytest.mark.parametrize("tokens", [1, 40, 128 * 160])
+def test_token_attn_nan_that_is_seen(cuda_lib, fp8, tokens):
+    """Keys that are all NaN, in a list of one CTA, of a cluster, and of several
+    clusters: the result is NaN, not that of a query that sees nothing."""
+    import torch
+    wave = cuda_lib
+    kv = _cache(wave, 1, 64, tokens, 1, pages=(tokens + 127) // 128, fp8=fp8)
+    k = torch.full((tokens, 1, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(k)
+    kv.append(0, 1, k, v)
+    if fp8:  # the append's codes of NaN are its own matter: set E4M3's
+        pb, off, _ = kv.layout()
+        codes = kv.pool[off:].view(torch.uint8)
+        for p in kv.entry_pages(0, 1):
+            codes[p * pb:(p + 1) * pb].view(2, 128, 64)[0] = 0x7F
+    q = torch.ones(2, 1, 64, dtype=torch.bfloat16, device="cuda")
+    O, lse = torch.zeros_like(q), torch.zeros(2, 1, device="cuda")
+    nodes, own = [(0, 1)] * 2, [tokens, 0]
+    ws = torch.empty(max(1, kv.token_attn_workspace(nodes, "same", own)), dtype=torch.uint8, device="cuda")
+    kv.token_attn(nodes, "same", q, O, own_tokens=own, lse=lse, workspace=ws)
+    kv.status()
+    assert torch.isnan(O[0]).all() and torch.isnan(lse[0]).all()
+    assert (O[1] == 0).all() and torch.isneginf(lse[1]).all()
+
+
+@FORMATS
 def test_token_attn_large_and_small_values(cuda_lib, fp8):
     """Peaked weights and magnitudes far from 1 (keys and values of 2^40 and 2^-40)."""
     import torch
@@ -679,6 +722,59 @@ def test_token_ops_in_a_graph_on_a_side_stream(cuda_lib):
         step()
         torch.cuda.synchronize()
         assert torch.equal(replayed, O), f"replay {i}"
+    del graph
+
+
+def test_captured_across_streams_and_other_nodes(cuda_lib):
+    """A capture whose launches follow a fill, a copy, another library's kernel and a
+    join of two streams (a launch that may start early is captured as an edge of
+    its own kind, from each of these)."""
+    import torch
+    w = _World(cuda_lib, 2, 64, 200, 1, seed=15, pages=40)
+    for c in range(4):
+        w.add(c, 1)
+    kv, nodes = w.kv, [(3, 1)]
+    A, B = (_dev(_bf(w.rng, 40, 128)) for _ in range(2))
+    W = _dev(_bf(w.rng, 128, 128, scale=0.1))
+    X, Y, Z, O = (torch.empty(40, 128, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    pos = torch.zeros(40, 3, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(1, kv.token_attn_workspace(nodes, "same", [200])), dtype=torch.uint8, device="cuda")
+    other = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        Y.zero_()
+        kv.linear_bias(A, W, X, R=Y)                       # after a fill
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            kv.linear_bias(B, W, Z)                        # after the fork
+            kv.rotary(pos, Z.view(40, 2, 64))
+        kv.rotary(pos, X.view(40, 2, 64))
+        here.wait_stream(other)
+        kv.linear_bias(X, W, Y, R=Z)                       # after the join
+        X.copy_(Y)
+        kv.rotary(pos, X.view(40, 2, 64), inverse=True)    # after a copy
+        X.mul_(0.5)
+        O.zero_()
+        kv.token_attn(nodes, "same", X.view(40, 2, 64)[:1], O.view(40, 2, 64)[:1], own_tokens=[200], workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    want = [t.clone() for t in (X, Y, Z, O)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(20):
+        for t in (X, Y, Z, O):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (X, Y, Z, O)))
+    kv.status()
     del graph
 
 
