@@ -10,13 +10,24 @@
 namespace wavei {
 namespace {
 
-// Up to 16 rows: token_rows_kernel (wave_few.cu). Blocks of 16 features where they
-// still give every SM two (one token, us: 1536 -> 8960 7.8, 8-feature blocks 8.4;
-// 1536 -> 1536 5.0 and 3.9); 16 warps to a block where K is long and the blocks
-// few (8960 -> 1536: 10.0, with 8 warps 12.5; 1536 -> 1536: 4.4 and 3.9).
+// Up to 16 rows: token_rows_kernel (wave_few.cu), by waves of its blocks: an SM holds
+// four of 8 warps (three with more than 8 rows), two of 16. Blocks of 8 features while
+// they are one wave, else of 16 (chained, weights from HBM, us, 8 and 16 features: 1536
+// -> 1536 3.2 and 4.3, 2048 -> 4736 4.7 and 6.0, 1536 -> 6144 6.6 and 5.6, 1536 -> 8960
+// 7.3 and 6.3, 8192 -> 8192 25.8 and 26.8). Sixteen warps to a block where that is one
+// wave and K is long (8 and 16 warps: 8960 -> 1536 11.2 and 8.4, 4096 -> 2048 5.7 and
+// 4.6, 2048 -> 1536 3.1 and 3.4, 4096 -> 4096 7.4 and 9.0).
+// With 9 to 16 rows a block reads more of A than of W, and tiles of 64 features take
+// over beyond one wave or where K is long (token rows and tiles: 16 rows 1536 -> 4608
+// 5.9 and 7.2, 4096 -> 4096 11.4 both, 8960 -> 1536 14.1 and 10.6, 8192 -> 8192 38.9
+// and 28.8; 12 rows 1536 -> 8960 9.8 and 8.4, 4096 -> 2048 6.9 and 8.5).
+bool takes_tokens(const wave_kv* kv, const DenseArgs& a) {
+  return a.M <= 8 || (a.M <= 16 && a.K <= 4096 && a.N <= 3 * 16 * kv->num_sms);
+}
 int launch_tokens(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
-  if (a.N >= 2 * 16 * kv->num_sms) return token_rows_launch(a, 2, 8, s);
-  return token_rows_launch(a, 1, a.K >= 4096 && a.M <= 8 ? 16 : 8, s);
+  const int held = a.M <= 8 ? 4 : 3;
+  if (a.N > held * 8 * kv->num_sms) return token_rows_launch(a, 2, 8, s);
+  return token_rows_launch(a, 1, a.M <= 8 && a.K >= 4096 && a.N <= 2 * 8 * kv->num_sms ? 16 : 8, s);
 }
 
 // More rows: the cheapest form by its cost in us: a start and end, more where the
@@ -100,5 +111,5 @@ extern "C" int wave_linear_bias(wave_kv* kv, const void* A, int64_t lda, int32_t
   const DenseArgs a{A, lda, M, K, W, N, static_cast<const uint16_t*>(bias), static_cast<const uint16_t*>(R),
                     ldr, act, static_cast<uint16_t*>(Y), ldy};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return M <= 16 ? launch_tokens(kv, a, s) : launch_rows(kv, a, s);
+  return takes_tokens(kv, a) ? launch_tokens(kv, a, s) : launch_rows(kv, a, s);
 }

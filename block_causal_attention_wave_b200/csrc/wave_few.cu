@@ -49,6 +49,7 @@ struct TokenRowsParams {
   const uint16_t* bias;
   int64_t lda, ldr, ldy;
   int32_t M, K, N;
+  int32_t ahead;  // bytes of each weight row that go into L2 before chain_wait
 };
 
 // 16 bytes, or zeros without a load (predicated, so that a batch of loads stays
@@ -71,6 +72,10 @@ __device__ __forceinline__ uint4 ld_rows(const uint16_t* p, bool in) {
       : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)in));
   return v;
 }
+// `bytes` (a multiple of 16, as `p` is aligned) on their way into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -85,10 +90,21 @@ __global__ void __launch_bounds__(32 * WARPS) token_rows_kernel(const __grid_con
   constexpr int U = FT == 1 ? 4 : 2;  // chunks of K in a batch
   __shared__ float red[WARPS][16][8 * FT];
   chain_begin();
-  chain_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r8 = lane >> 2, q4 = lane & 3;
   const int f0 = blockIdx.x * 8 * FT;
+  {
+    // While the kernel before still runs, the weights are sent for: into L2, which a
+    // write by that kernel would reach too, and not read. Thread t: piece t % pieces
+    // of row t / pieces.
+    const int rows = min(8 * FT, p.N - f0), pieces = (p.ahead + 2047) >> 11;
+    const char* w = reinterpret_cast<const char*>(p.w + (int64_t)f0 * p.K);
+    for (int t = threadIdx.x; t < rows * pieces; t += 32 * WARPS) {
+      const int r = t / pieces, at = (t - r * pieces) << 11;
+      prefetch_l2(w + (int64_t)r * p.K * 2 + at, (uint32_t)min(2048, p.ahead - at));
+    }
+  }
+  chain_wait();
   const uint16_t* wrow[FT];
   bool win[FT];
 #pragma unroll
@@ -394,8 +410,13 @@ int launch_split_act(const SplitParams& p, int tiles, int act, int device, cudaS
 }  // namespace
 
 int token_rows_launch(const DenseArgs& a, int ft, int warps, cudaStream_t s) {
+  // Ahead of the wait go 16 MB in all, of each row its first part (chained, cold, us,
+  // with none / 4 / 16 / 64 MB: 1536 -> 8960 7.2 / 6.5 / 6.3 / 6.7; 8960 -> 1536 9.3 /
+  // 8.8 / 8.3 / 8.1; 8192 -> 8192 26.8 / 26.5 / 26.7 / 28.3; a block's whole step of
+  // seven calls 48.4 / 47.4 / 46.7 / 48.8).
+  const int64_t ahead = std::min<int64_t>(2LL * a.K, (16 << 20) / a.N & ~15);
   const TokenRowsParams p{static_cast<const uint16_t*>(a.A), static_cast<const uint16_t*>(a.W), a.Y, a.R, a.bias,
-                          a.lda, a.ldr, a.ldy, a.M, a.K, a.N};
+                          a.lda, a.ldr, a.ldy, a.M, a.K, a.N, (int32_t)ahead};
   const bool r16 = a.M > 8;
   const cudaError_t e =
       warps == 16 ? launch_token_rows<16, 1, false>(p, a.act, s)

@@ -124,6 +124,13 @@ def test_linear_block_sizes(cuda_lib, M, K, N):
     _linear_case(cuda_lib, kv, np.random.default_rng(13), M, K, N, "gelu_tanh", True, True)
 
 
+@pytest.mark.parametrize("M,K,N", [(8, 1536, 5000), (3, 2048, 4736), (5, 4096, 2368), (5, 4096, 2376), (9, 1536, 3552),
+                                   (16, 1000, 3560), (16, 4096, 7104), (16, 4104, 520), (9, 264, 7112), (12, 8960, 1536)])
+def test_linear_few_rows_by_waves(cuda_lib, M, K, N):
+    """Both sides of each limit between the forms for up to 16 rows."""
+    _linear_case(cuda_lib, _cache(cuda_lib), np.random.default_rng(6), M, K, N, "silu", True, True, pad=16)
+
+
 def test_linear_no_rows(cuda_lib):
     import torch
     kv = _cache(cuda_lib)
