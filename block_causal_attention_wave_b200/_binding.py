@@ -3,7 +3,9 @@
 Every computation (scheduling, page allocation, key tables, the append and
 attention kernels) happens inside the C library; this module turns Python
 values and torch tensors into the plain pointers and sizes the C ABI takes.
-There is no fallback: if the library is missing, ``load()`` raises.
+There is no fallback: if the library is missing, ``load()`` raises. The calls of
+single tokens, where Python's time would exceed the GPU's, are marshalled by
+the extension module ``_call`` (csrc/py), which is built with the library.
 """
 from __future__ import annotations
 
@@ -191,6 +193,26 @@ def load(path: str = None) -> ctypes.CDLL:
     return lib
 
 
+_call = None
+
+
+def _bind_calls(lib):
+    """Give the extension module the C entries it calls (once)."""
+    global _call
+    if _call is not None:
+        return
+    import torch
+    try:
+        from . import _call as module
+    except ImportError as e:
+        raise RuntimeError("the module _call is missing: build it with "
+                           "`python -m block_causal_attention_wave_b200.build`") from e
+    module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                  for name in ("wave_linear_bias", "wave_rotary", "wave_kv_write_tokens",
+                               "wave_token_attn")), torch.bfloat16, torch.float32, torch.int32)
+    _call = module
+
+
 def exported_symbols():
     return list(_SIGS)
 
@@ -227,8 +249,7 @@ def _pairs(active):
 
 @functools.lru_cache(maxsize=256)
 def _rotary_spec(pairs, base, layout, ladder, inverse):
-    return ctypes.pointer(RotarySpec(pairs, base, ROTARY_LAYOUTS[layout], ROTARY_LADDERS[ladder],
-                                     inverse))
+    return RotarySpec(pairs, base, ROTARY_LAYOUTS[layout], ROTARY_LADDERS[ladder], inverse)
 
 
 def _stream_handle(stream):
@@ -318,6 +339,7 @@ class KVCache:
         h = ctypes.c_void_p()
         _check(self.lib.wave_kv_create(ctypes.byref(cfg), ctypes.byref(h)))
         self.h = h
+        self._handle = h.value
 
     @staticmethod
     def page_bytes(heads, head_dim, kv_format=0) -> int:
@@ -333,7 +355,7 @@ class KVCache:
     def close(self):
         if getattr(self, "h", None):
             self.lib.wave_kv_destroy(self.h)
-            self.h = None
+            self.h = self._handle = None
 
     def __del__(self):
         try:
@@ -404,24 +426,6 @@ class KVCache:
                                     _stream_handle(stream)))
         return Y
 
-    def _rows(self, t, what, rows, width, dtype=None):
-        """(address, row stride) of a CUDA tensor read as ``rows`` rows of
-        ``width`` contiguous elements: 2-D [rows][width], or [rows][heads][d]
-        with contiguous heads. A kernel would read a host tensor's address, or
-        past a short one, as readily as a good one, so both are refused here."""
-        shape, stride = t.shape, t.stride()
-        if len(shape) == 3:
-            ok = (shape[1] * shape[2] == width and stride[2] == 1
-                  and (stride[1] == shape[2] or shape[1] == 1))
-        else:
-            ok = len(shape) == 2 and shape[1] == width and stride[1] == 1
-        if not (ok and shape[0] == rows and t.dtype is (dtype or self._bf16)
-                and t.get_device() == self._index):
-            raise ValueError(f"{what}: {rows} rows of {width} contiguous {dtype or self._bf16} "
-                             f"elements on cuda:{self._index} are wanted, got shape {tuple(shape)}, "
-                             f"strides {tuple(stride)}, {t.dtype} on {t.device}")
-        return t.data_ptr(), stride[0] if rows > 1 else width
-
     def _stream(self, stream):
         """A cudaStream_t: the given one, or torch's current stream of the pool's
         device (read without building a Stream object, which costs 3 us)."""
@@ -430,14 +434,13 @@ class KVCache:
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     def _device(self):
-        if self._index is None:
-            if self.pool is None:
-                raise WaveError(ERR_ARG, "host-only handle (pool == NULL)")
-            import torch
-            self._index, self._bf16 = self.pool.get_device(), torch.bfloat16
-            self._f32, self._i32 = torch.float32, torch.int32
-            self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-                lambda i: torch.cuda.current_stream(i).cuda_stream)
+        if self.pool is None:
+            raise WaveError(ERR_ARG, "host-only handle (pool == NULL)")
+        import torch
+        _bind_calls(self.lib)
+        self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+        self._index = self.pool.get_device()
 
     def linear_bias(self, A, W, Y, bias=None, R=None, act="none", stream=None):
         """Y [M][N] = act(A W^T + bias) (+ R) for A [M][K], W [N][K], bias [N], R
@@ -445,24 +448,11 @@ class KVCache:
         ``act``: "none", "gelu_tanh", "gelu_erf" or "silu" (or an ACT_* code)."""
         if self._index is None:
             self._device()
-        M, K = A.shape
-        N = W.shape[0]
-        a, lda = self._rows(A, "A", M, K)
-        w, ldw = self._rows(W, "W", N, K)
-        y, ldy = self._rows(Y, "Y", M, N)
-        if N > 1 and ldw != K:
-            raise ValueError("W must be contiguous")
-        b = None
-        if bias is not None:
-            if (bias.dtype is not self._bf16 or bias.get_device() != self._index
-                    or bias.numel() != N or not bias.is_contiguous()):
-                raise ValueError(f"bias: {N} contiguous {self._bf16} elements on "
-                                 f"cuda:{self._index} are wanted")
-            b = bias.data_ptr()
-        r, ldr = self._rows(R, "R", M, N) if R is not None else (None, 0)
-        code = ACTIVATIONS[act] if isinstance(act, str) else int(act)
-        _check(self.lib.wave_linear_bias(self.h, a, lda, M, K, w, N, b, r, ldr, code, y, ldy,
-                                         self._stream(stream)))
+        rc = _call.linear_bias(self._handle, self._index, A, W, Y, bias, R,
+                               ACTIVATIONS[act] if isinstance(act, str) else int(act),
+                               self._stream(stream))
+        if rc:
+            _check(rc)
         return Y
 
     def rotary(self, positions, Q, K=None, Qout=None, Kout=None, pairs=None, base=10000.0,
@@ -475,30 +465,18 @@ class KVCache:
         turn back, which is the gradient of turning."""
         if self._index is None:
             self._device()
-        rows, d = Q.shape[0], self.head_dim
         if pairs is None:
+            d = self.head_dim
             pairs = (d // 2 - 2 * (d // 6), d // 6, d // 6)
-        if Q.shape[-1] != d or (K is not None and K.shape[-1] != d):
-            raise ValueError(f"Q and K are [rows][heads][{d}]")
         if Qout is None:
             Qout = Q
-        if K is not None and Kout is None:
+        if Kout is None:
             Kout = K
-        p, ldp = self._rows(positions, "positions", rows, 3, self._i32)
-        if rows > 1 and ldp != 3:
-            raise ValueError("positions must be contiguous")
-        qh = Q.shape[1]
-        q, ldq = self._rows(Q, "Q", rows, qh * d)
-        qo, ldqo = self._rows(Qout, "Qout", rows, qh * d)
-        k = ko = None
-        ldk = ldko = kh = 0
-        if K is not None:
-            kh = K.shape[1]
-            k, ldk = self._rows(K, "K", rows, kh * d)
-            ko, ldko = self._rows(Kout, "Kout", rows, kh * d)
         spec = _rotary_spec(tuple(pairs), base, layout, ladder, bool(inverse))
-        _check(self.lib.wave_rotary(self.h, spec, p, rows, q, ldq, qh, qo, ldqo, k,
-                                    ldk, kh, ko, ldko, self._stream(stream)))
+        rc = _call.rotary(self._handle, self._index, self.head_dim, ctypes.addressof(spec), positions,
+                          Q, K, Qout, Kout, self._stream(stream))
+        if rc:
+            _check(rc)
         return (Qout, Kout) if K is not None else Qout
 
     def write_tokens(self, entries, first, K, V, counts=None, stream=None):
@@ -507,14 +485,10 @@ class KVCache:
         (``counts``: one each by default). Entries need pages (alloc)."""
         if self._index is None:
             self._device()
-        n = len(entries)
-        counts = [1] * n if counts is None else counts
-        width, rows = self.heads * self.head_dim, sum(counts)
-        k, ldk = self._rows(K, "K", rows, width)
-        v, ldv = self._rows(V, "V", rows, width)
-        _check(self.lib.wave_kv_write_tokens(self.h, n, _pairs(entries), _ints(first, n, "first"),
-                                             _ints(counts, n, "counts"), k, ldk, v, ldv,
-                                             self._stream(stream)))
+        rc = _call.write_tokens(self._handle, self._index, self.heads * self.head_dim, entries,
+                                first, counts, K, V, self._stream(stream))
+        if rc:
+            _check(rc)
 
     def token_attn_workspace(self, active, policy, own_tokens=None, q_heads=None) -> int:
         """Workspace bytes that token_attn needs for these arguments (may be 0)."""
@@ -533,23 +507,10 @@ class KVCache:
         ``workspace`` is a CUDA tensor of token_attn_workspace() bytes."""
         if self._index is None:
             self._device()
-        n = len(active)
-        q_heads = Q.shape[1]
-        own = _ints(own_tokens, n, "own_tokens") if own_tokens is not None else None
-        q, ldq = self._rows(Q, "Q", n, q_heads * self.head_dim)
-        o, ldo = self._rows(O, "O", n, q_heads * self.head_dim)
-        s = None
-        if lse is not None:
-            s, lds = self._rows(lse, "lse", n, q_heads, self._f32)
-            if n > 1 and lds != q_heads:
-                raise ValueError("lse must be contiguous")
-        ws, nbytes = None, 0
-        if workspace is not None:
-            if workspace.get_device() != self._index or not workspace.is_contiguous():
-                raise ValueError(f"workspace: a contiguous tensor on cuda:{self._index} is wanted")
-            ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        _check(self.lib.wave_token_attn(self.h, _pairs(active), n, _policy(policy), own, q_heads, q,
-                                        ldq, o, ldo, s, ws, nbytes, self._stream(stream)))
+        rc = _call.token_attn(self._handle, self._index, self.head_dim, active, _policy(policy), Q, O,
+                              own_tokens, lse, workspace, self._stream(stream))
+        if rc:
+            _check(rc)
         return O
 
     def release(self, chunk, level):

@@ -1,4 +1,4 @@
-"""Build libwave.so in-tree with nvcc for sm_100a.
+"""Build libwave.so in-tree with nvcc for sm_100a, and the binding's extension module.
 
 Usage: ``python -m block_causal_attention_wave_b200.build [--verbose-ptxas]``.
 Compiles every ``csrc/*.cu`` / ``csrc/*.cpp`` into one shared library next to
@@ -12,10 +12,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libwave.so")
+CALL = os.path.join(PKG, "_call.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -63,7 +65,23 @@ def build(verbose_ptxas: bool = False, out: str = LIB, defines=(), replace=None)
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("link of libwave.so failed")
     os.replace(tmp, out)
+    if out == LIB:
+        build_call()
     return out
+
+
+def build_call() -> str:
+    """Compile the binding's extension module (csrc/py), which needs Python's
+    headers and neither CUDA nor libwave.so."""
+    cmd = [shutil.which("g++") or "g++", "-O2", "-Wall", "-std=c++17", "-shared", "-fPIC",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"),
+           os.path.join(PKG, "csrc", "py", "wave_call.cpp"), "-o", CALL + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=300)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on wave_call.cpp")
+    os.replace(CALL + ".tmp", CALL)
+    return CALL
 
 
 if __name__ == "__main__":
