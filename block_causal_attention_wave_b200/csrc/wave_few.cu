@@ -11,11 +11,12 @@
 // contracted index is free, so a lane's eight consecutive k serve two MMAs),
 // rows of A likewise. A block takes 8 FT features; its 8 or 16 warps take
 // neighbouring 32-wide chunks of K, and their sums meet in shared memory in a
-// fixed order.
+// fixed order. One token, 1536 -> 8960: 4.8 us back to back, 6.3 (4.4 TB/s) with its
+// 27.5 MB of weights from HBM; 8192 -> 8192 26.8 (5.0 TB/s).
 //
 // split_rows_kernel, more rows. Tiles of 128 rows x NF features on tcgen05, K
 // cut over the CTAs of a cluster (any number up to 8) until the tiles fill the
-// SMs; each CTA streams its share of K through a TMA ring of up to 192 KB,
+// SMs; each CTA streams its share of K through a TMA ring of 192 KB, 128 of K a stage,
 // accumulates in TMEM, and the partial tiles are summed through distributed
 // shared memory in rank order: no workspace, no atomics, one launch. 192
 // threads: warp 0 lane 0 TMA, warp 1 lane 0 tcgen05, warps 2..5 the epilogue.

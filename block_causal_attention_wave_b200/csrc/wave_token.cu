@@ -34,7 +34,7 @@
 //     S^T = K Q^T (16 keys x 8 query rows) and O^T += V^T P^T (16 d x 8 query
 //     rows), QT = 1 or 2 tiles of query rows. With the queries as the sixteen rows
 //     one token filled one of them: twice the MMAs, exponentials and registers
-//     (32 FP8 units: 50.7 us, this way 40.8).
+//     (32 FP8 units: 50.7 us, this way 40.8, and 38.1 with launches chained).
 //   - Within an MMA the order of the contracted index, and which d is which row,
 //     are free, so a lane's operand is whole 16-byte vectors of a token's row, all
 //     conflict-free under the swizzle; P is turned into its operand's layout by
