@@ -906,3 +906,115 @@ def test_token_attn_many_calls_back_to_back(cuda_lib, fp8, d):
         kv.token_attn(nodes, "same", q, o, own_tokens=own, workspace=ws)
     kv.status()
     assert torch.isfinite(outs[0].float()).all() and all(torch.equal(o, outs[0]) for o in outs)
+
+
+# ---------------------------------------------- what lies beside the outputs
+@pytest.mark.parametrize("M,K,N", [(1, 64, 24), (13, 264, 520), (37, 1000, 1544), (300, 72, 200), (984, 4096, 1536),
+                                   (1500, 200, 776), (4000, 136, 1544)])
+def test_rows_around_a_dense_layer_stay(cuda_lib, M, K, N):
+    """Rows before and behind Y, and columns beside it, in every form."""
+    import torch
+    kv, rng = _cache(cuda_lib), np.random.default_rng(21)
+    a, w = _bf(rng, M, K), _bf(rng, N, K, scale=K ** -0.5)
+    big = torch.full((M + 300, N + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+    Y = big[150:150 + M, 8:8 + N]
+    kv.linear_bias(_dev(a), _dev(w), Y, act="silu")
+    kv.status()
+    want = otok.linear_bias(a, w, None, None, "silu")
+    size = np.abs(a) @ np.abs(w).T
+    _within(torch_to_f64(Y), want, (U + 2.0 ** -14) * np.abs(want) + (2 * K + 16) * 2.0 ** -23 * size)
+    Y.fill_(7.0)
+    assert (big == 7.0).all()
+
+
+@FORMATS
+def test_rows_around_the_other_outputs_stay(cuda_lib, fp8):
+    """Rows behind rotated ones, behind O and lse; pages of other entries, and the pool
+    around them, under a write."""
+    import torch
+    H, d = 3, 64
+    w = _World(cuda_lib, H, d, 300, 1, fp8=fp8, seed=22)
+    for c in range(3):
+        w.add(c, 1)
+    kv = w.kv
+    big = torch.full((90, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    pos = torch.randint(-9, 9, (77, 3), dtype=torch.int32, device="cuda")
+    kv.rotary(pos, torch.ones(77, H, d, dtype=torch.bfloat16, device="cuda"), Qout=big[5:82])
+    assert (big[:5] == 7.0).all() and (big[82:] == 7.0).all() and not (big[5:82] == 7.0).any()
+    big.fill_(7.0)
+    lse = torch.full((90, H), 7.0, device="cuda")
+    nodes, own = [(2, 1)] * 3, [300, 1, 0]
+    ws = torch.empty(max(1, kv.token_attn_workspace(nodes, "same", own)), dtype=torch.uint8, device="cuda")
+    kv.token_attn(nodes, "same", torch.ones(3, H, d, dtype=torch.bfloat16, device="cuda"), big[5:8], own_tokens=own,
+                  lse=lse[5:8], workspace=ws)
+    for t in (big, lse):
+        assert (t[:5] == 7.0).all() and (t[8:] == 7.0).all() and not (t[5:8] == 7.0).any()
+    pb, off, _ = kv.layout()
+    before = kv.pool.clone()
+    x = _dev(_bf(w.rng, 2, H, d))
+    kv.write_tokens([(1, 1)], [200], x, x, [2])
+    kv.status()
+    changed = (kv.pool != before).nonzero().flatten().cpu().numpy()
+    page = kv.entry_pages(1, 1)[1]
+    scales = range(0)
+    if fp8:
+        at = kv.scale_offset() + page * 2 * H * 4
+        scales = range(at, at + 2 * H * 4)
+    own_bytes = np.array([off + page * pb <= i < off + (page + 1) * pb or i in scales for i in changed])
+    assert changed.size and own_bytes.all()
+
+
+def test_two_threads_with_a_handle_each(cuda_lib):
+    """Calls of two threads at once, on their own handles and streams, give what one
+    thread's calls give."""
+    import threading
+
+    import torch
+    worlds = [_World(cuda_lib, 2, 64, 300, 1, fp8=fp8, seed=23 + fp8, pages=40) for fp8 in (False, True)]
+    for w in worlds:
+        for c in range(4):
+            w.add(c, 1)
+
+    def steps(w, out):
+        kv, gen = w.kv, torch.Generator(device="cuda").manual_seed(5)
+        X = torch.randn(300, 128, generator=gen, device="cuda").bfloat16()
+        W = torch.randn(128, 128, generator=gen, device="cuda").bfloat16()
+        pos = torch.arange(900, device="cuda", dtype=torch.int32).view(300, 3)
+        Y, O = torch.empty_like(X), torch.empty(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+        nodes = [(3, 1)]
+        ws = torch.empty(max(1, kv.token_attn_workspace(nodes, "same", [300])), dtype=torch.uint8, device="cuda")
+        for i in range(60):
+            M = (1, 20, 300)[i % 3]
+            kv.linear_bias(X[:M], W, Y[:M], act="silu")
+            kv.rotary(pos[:M], Y[:M].view(M, 2, 64))
+            kv.write_tokens([(3, 1)], [i], Y[:1].view(1, 2, 64), Y[:1].view(1, 2, 64))
+            kv.token_attn(nodes, "same", Y[:1].view(1, 2, 64), O, own_tokens=[300], workspace=ws)
+            out.append((Y[:M].clone(), O.clone()))
+
+    def run(w, out, errors):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                steps(w, out)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    torch.cuda.synchronize()
+    pools, errors, alone, together = [w.kv.pool.clone() for w in worlds], [], [[], []], [[], []]
+    for w, out in zip(worlds, alone):
+        run(w, out, errors)
+    torch.cuda.synchronize()
+    for w, p in zip(worlds, pools):
+        w.kv.pool.copy_(p)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(w, out, errors)) for w, out in zip(worlds, together)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    torch.cuda.synchronize()
+    assert not errors and all(len(o) == 60 for o in together)
+    for a, b in zip(alone, together):
+        for (y, o), (yy, oo) in zip(a, b):
+            assert torch.equal(y, yy) and torch.equal(o, oo)
+    for w in worlds:
+        w.kv.status()
