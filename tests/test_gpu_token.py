@@ -1018,3 +1018,36 @@ def test_two_threads_with_a_handle_each(cuda_lib):
             assert torch.equal(y, yy) and torch.equal(o, oo)
     for w in worlds:
         w.kv.status()
+
+
+def test_chained_launches_wait_for_events(cuda_lib):
+    """A launch that may start before the kernel ahead of it in its stream has ended
+    still starts behind an event of another stream, whose work is late."""
+    import torch
+    w = _World(cuda_lib, 2, 64, 200, 1, seed=25)
+    w.add(0, 1)
+    kv, other = w.kv, torch.cuda.Stream()
+    W = torch.eye(128, device="cuda").bfloat16()
+    pos = torch.zeros(300, 3, dtype=torch.int32, device="cuda")
+    K = torch.ones(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    own, O = [200], torch.empty_like(K)
+    ws = torch.empty(max(1, kv.token_attn_workspace([(0, 1)], "same", own)), dtype=torch.uint8, device="cuda")
+    for M in (1, 40, 300):
+        X, T = (torch.zeros(M, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        Y, Z = torch.empty_like(X), torch.empty_like(X)
+        for i in range(1, 9):
+            here = torch.cuda.current_stream()
+            other.wait_stream(here)
+            with torch.cuda.stream(other):
+                torch.cuda._sleep(200000)
+                X.fill_(float(i))
+                K.fill_(float(i))
+                kv.linear_bias(X, W, T)
+            kv.linear_bias(Z.zero_(), W, Y)             # a kernel just ahead of the wait
+            here.wait_stream(other)
+            kv.linear_bias(T, W, Y)
+            kv.rotary(pos[:M], Y.view(M, 2, 64), Qout=Z.view(M, 2, 64))
+            kv.write_tokens([(0, 1)], [0], K, K)
+            kv.token_attn([(0, 1)], "same", K, O, own_tokens=[1], workspace=ws)
+            assert (T == i).all() and (Y == i).all() and (Z == i).all() and (O == i).all(), (M, i)
+    kv.status()
