@@ -427,7 +427,10 @@ int wave_round_attn_split_workspace(wave_kv* kv, const wave_node* active, int32_
  * results over parts of a cache can be joined. Strides in elements, multiples
  * of 8, >= q_heads * d; 16-byte aligned pointers (lse: 4). O overlaps nothing.
  * bf16 and FP8 pools: an FP8 page is read in place, its values code * s in
- * float32 without the rounding to bf16 of wave_round_attn_split.
+ * float32 without the rounding to bf16 of wave_round_attn_split. A token's weight keeps
+ * at least 15 bits in its product with V (bf16 pools; wave_round_attn rounds it to bf16) or
+ * 11 (FP8 pools, whose codes have 4); scores, sums and results before their one
+ * rounding are float32.
  * The key lists are cut over the GPU's SMs in pages and joined in the same
  * launch (a few long lists in a second one, through the workspace); a page that
  * several queries read is read once for up to 16 / (q_heads / H) of them that
