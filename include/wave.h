@@ -239,7 +239,9 @@ int wave_linear(wave_kv* kv, const void* A, int32_t M, int32_t K, const void* W,
 
 /* A dense layer with a bias, for any number of rows from one token up:
  * Y = act(A W^T + bias) (+ R), fp32 accumulation and epilogue, one rounding
- * to bf16. wave_linear is the form without bias for whole rounds; this one
+ * to bf16. Activations are good to 2^-14 of their value, their far negative ends
+ * included, down to where their factor of x leaves float32's normal range (2^-126)
+ * and the result is zero. wave_linear is the form without bias for whole rounds; this one
  * serves blocks whose projections carry a bias, widths that fill no tile, and
  * the single tokens that stream beside a round ([WS] "streaming unit").
  * A: device bf16, M rows of K, row stride lda; W: device bf16 [N][K],

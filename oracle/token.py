@@ -15,20 +15,21 @@ import math
 import numpy as np
 
 from . import quant
-from .block import gelu_tanh
 from .cache import key_entries
 
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def activation(x, act):
     x = np.asarray(x, dtype=np.float64)
     if act == "none":
         return x
-    if act == "gelu_tanh":
-        return gelu_tanh(x)
+    # Each in the form that loses nothing where its factor of x is small.
+    if act == "gelu_tanh":  # 0.5 (1 + tanh u) = 1 / (1 + e^(-2u))
+        with np.errstate(over="ignore"):
+            return x / (1.0 + np.exp(-2.0 * math.sqrt(2.0 / math.pi) * (x + 0.044715 * x ** 3)))
     if act == "gelu_erf":
-        return 0.5 * x * (1.0 + _erf(x / math.sqrt(2.0)))
+        return 0.5 * x * _erfc(-x / math.sqrt(2.0))
     if act == "silu":
         # x / (1 + e^-x), without overflow on either side
         e = np.exp(-np.abs(x))

@@ -69,3 +69,22 @@ def test_attention_takes_infinite_values(cuda_lib, T, at):
     q[..., 0] = 8.0
     got = _attend(cuda_lib, k, v, q, [T])[0]
     assert np.isposinf(got[:, :32]).all() and np.isneginf(got[:, 32:]).all()
+
+
+@pytest.mark.parametrize("M", [16, 400])
+@pytest.mark.parametrize("act,most", [("gelu_erf", 12.5), ("gelu_tanh", 10.0), ("silu", 80.0)])
+def test_activations_keep_their_tails(cuda_lib, act, most, M):
+    """One product a result, so that no sum's tolerance hides the activation: every
+    result is good to 2^-14 of itself and the one rounding, whatever its size."""
+    import torch
+    kv = _cache(cuda_lib)
+    x = oblock.bf16_round(np.linspace(-most, most, 2000))
+    w = np.zeros((2000, 8))
+    w[:, 0] = x
+    a = np.zeros((M, 8))
+    a[:, 0] = 1.0
+    Y = torch.empty(M, 2000, dtype=torch.bfloat16, device="cuda")
+    kv.linear_bias(_dev(a), _dev(w), Y, act=act)
+    kv.status()
+    ref = np.broadcast_to(otok.activation(x, act), (M, 2000))
+    _within(torch_to_f64(Y), ref, (U + 2.0 ** -14) * np.abs(ref), act)
