@@ -21,13 +21,11 @@ namespace {
 // over beyond one wave or where K is long (token rows and tiles: 16 rows 1536 -> 4608
 // 5.9 and 7.2, 4096 -> 4096 11.4 both, 8960 -> 1536 14.1 and 10.6, 8192 -> 8192 38.9
 // and 28.8; 12 rows 1536 -> 8960 9.8 and 8.4, 4096 -> 2048 6.9 and 8.5).
-bool takes_tokens(const wave_kv* kv, const DenseArgs& a) {
-  return a.M <= 8 || (a.M <= 16 && a.K <= 4096 && a.N <= 3 * 16 * kv->num_sms);
-}
-int launch_tokens(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
-  const int held = a.M <= 8 ? 4 : 3;
-  if (a.N > held * 8 * kv->num_sms) return token_rows_launch(a, 2, 8, s);
-  return token_rows_launch(a, 1, a.M <= 8 && a.K >= 4096 && a.N <= 2 * 8 * kv->num_sms ? 16 : 8, s);
+bool takes_tokens(int sms, int32_t M, int32_t K, int32_t N) { return M <= 8 || (M <= 16 && K <= 4096 && N <= 3 * 16 * sms); }
+DenseForm tokens_form(int sms, int32_t M, int32_t K, int32_t N) {
+  const int held = M <= 8 ? 4 : 3;
+  if (N > held * 8 * sms) return {kDenseTokens, 16, 8};
+  return {kDenseTokens, 8, M <= 8 && K >= 4096 && N <= 2 * 8 * sms ? 16 : 8};
 }
 
 // More rows: the cheapest form by its cost in us: a start and end, more where the
@@ -38,10 +36,8 @@ int launch_tokens(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
 // 256-column 34.5, 128-column tiles 38.6; 256 x 1536 x 1536: 64-column tiles with K
 // in two 8.4, 128-column in four 9.6, pairs 13; 512 x 1536 x 4608: 128-column tiles
 // 11.2, pairs 13.6; 2000 x 1536 x 8960: 256-column pairs 44, 192-column 50,
-// 128-column tiles 83. kHeld[c]: clusters of c CTAs that a B200 holds at a time
-// (occupancy query).
-int launch_rows(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
-  constexpr int kHeld[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+// 128-column tiles 83.
+DenseForm rows_form(int sms, int32_t M, int32_t K, int32_t N) {
   struct Form {
     int rows, cols, ctas, most;         // tile, CTAs that share one, most parts of K
     double start, join, slice, loaded;  // `loaded`: a slice in more than one wave
@@ -50,23 +46,22 @@ int launch_rows(const wave_kv* kv, const DenseArgs& a, cudaStream_t s) {
                               {128, 128, 1, 8, 5.3, 3.5, 0.49, 0.49},
                               {256, 192, 2, 4, 6.7, 3.5, 0.55, 0.62},
                               {256, 256, 2, 4, 8.2, 3.5, 0.60, 0.72}};
-  const int64_t slices = (a.K + 127) / 128;
+  const int64_t slices = (K + 127) / 128;
   double best = 1e30;
-  int form = 3, parts = 1;
+  DenseForm form{kDensePairs, 256, 1};
   for (int f = 0; f < 4; ++f)
     for (int n = 1; n <= kForms[f].most && n <= slices; ++n) {
       const Form& x = kForms[f];
-      const int64_t tiles = ((int64_t)a.M + x.rows - 1) / x.rows * ((a.N + x.cols - 1) / x.cols);
-      const int64_t held = std::max(1, kHeld[x.ctas * n] * kv->num_sms / 148);
+      const int64_t tiles = ((int64_t)M + x.rows - 1) / x.rows * ((N + x.cols - 1) / x.cols);
+      const int64_t held = clusters_held(x.ctas * n, sms);
       const double waves = (double)((tiles + held - 1) / held);
       // Pairs that do not share K are persistent: their tiles follow without a gap.
       const bool persistent = x.ctas == 2 && n == 1;
       const double t = (persistent ? 1.0 : waves) * (x.start + (n > 1 ? x.join : 0.0)) +
                        waves * (double)((slices + n - 1) / n) * (waves > 1 ? x.loaded : x.slice);
-      if (t < best) best = t, form = f, parts = n;
+      if (t < best) best = t, form = {x.ctas == 2 ? kDensePairs : kDenseTiles, x.cols, n};
     }
-  if (kForms[form].ctas == 2) return pair_rows_launch(kv, a, kForms[form].cols, parts, s);
-  return split_rows_launch(kv, a, kForms[form].cols, parts, s);
+  return form;
 }
 
 }  // namespace
@@ -83,6 +78,10 @@ int allow_shared(const void* fn, int bytes, int device, std::atomic<uint64_t>& d
 }  // namespace wavei
 
 using namespace wavei;
+
+extern "C" void wavei_dense_form(int32_t sms, int32_t M, int32_t K, int32_t N, DenseForm* form) {
+  *form = takes_tokens(sms, M, K, N) ? tokens_form(sms, M, K, N) : rows_form(sms, M, K, N);
+}
 
 extern "C" int wave_linear_bias(wave_kv* kv, const void* A, int64_t lda, int32_t M, int32_t K,
                                 const void* W, int32_t N, const void* bias, const void* R,
@@ -111,5 +110,8 @@ extern "C" int wave_linear_bias(wave_kv* kv, const void* A, int64_t lda, int32_t
   const DenseArgs a{A, lda, M, K, W, N, static_cast<const uint16_t*>(bias), static_cast<const uint16_t*>(R),
                     ldr, act, static_cast<uint16_t*>(Y), ldy};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return takes_tokens(kv, a) ? launch_tokens(kv, a, s) : launch_rows(kv, a, s);
+  DenseForm f;
+  wavei_dense_form(kv->num_sms, M, K, N, &f);
+  if (f.kind == kDenseTokens) return token_rows_launch(a, f.cols / 8, f.parts, s);
+  return f.kind == kDensePairs ? pair_rows_launch(kv, a, f.cols, f.parts, s) : split_rows_launch(kv, a, f.cols, f.parts, s);
 }

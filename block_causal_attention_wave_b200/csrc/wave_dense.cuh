@@ -181,6 +181,14 @@ inline bool wide_rows(const uint16_t* y, int64_t ldy) {
 // a bit per device.
 int allow_shared(const void* fn, int bytes, int device, std::atomic<uint64_t>& done);
 
+// The kernel that takes a call of wave_linear_bias, by its sizes alone.
+enum : int32_t { kDenseTokens = 0, kDenseTiles = 1, kDensePairs = 2 };
+struct DenseForm {
+  int32_t kind;
+  int32_t cols;   // features of a block (tokens) or columns of a tile
+  int32_t parts;  // warps of a block (tokens) or parts that K is cut into
+};
+
 // A checked call of wave_linear_bias.
 struct DenseArgs {
   const void* A;
@@ -212,3 +220,7 @@ int split_rows_launch(const struct ::wave_kv* kv, const DenseArgs& a, int nf, in
 int pair_rows_launch(const struct ::wave_kv* kv, const DenseArgs& a, int nt, int splits, cudaStream_t s);
 
 }  // namespace wavei
+
+// The choice on a GPU of `sms` SMs. Host only; C linkage, so that a test can ask
+// which form its sizes reach.
+extern "C" void wavei_dense_form(int32_t sms, int32_t M, int32_t K, int32_t N, wavei::DenseForm* form);

@@ -5,6 +5,7 @@
 #include <cuda.h>  // CUtensorMap (type only; the driver is reached at run time)
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled (type only)
 
+#include <algorithm>
 #include <cstdint>
 #include <map>
 #include <set>
@@ -68,6 +69,13 @@ int check_query_node(const wave_kv* kv, wave_node node);
 // code can meet).
 inline int no_host_memory() { return fail(WAVE_ERR_CAPACITY, "out of host memory"); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Clusters of `ctas` CTAs (1 .. 8, one CTA per SM) that a GPU of `sms` SMs holds at a
+// time: a B200's by occupancy query, others in proportion.
+inline int64_t clusters_held(int ctas, int sms) {
+  constexpr int kHeld[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+  return std::max(1, kHeld[ctas] * sms / 148);
+}
 
 // Device halves (defined in .cu files).
 int device_init(wave_kv* kv);
