@@ -5,11 +5,15 @@ import ctypes
 TOKENS, TILES, PAIRS = 0, 1, 2
 SMS = 148
 
-# (kind, columns of a tile, parts of K): sizes M, K, N. None of them fills a tile: the
+# (kind, columns of a tile, parts of K), of the few-row kernel (kind, features of a block,
+# warps): sizes M, K, N. None of them fills a tile: the
 # last rows' tile holds one row, a few, or most of its rows (pairs: with and without
 # rows for its odd half), parts of K and shares of rows are uneven, and the persistent
 # pairs' third size gives each more than two tiles.
 FORMS = {
+    (TOKENS, 8, 8): [(1, 216, 72), (8, 1032, 2376), (16, 200, 3544), (11, 4040, 1000)],
+    (TOKENS, 8, 16): [(1, 4104, 72), (8, 8968, 1544), (5, 4096, 2368)],
+    (TOKENS, 16, 8): [(1, 200, 4744), (8, 4104, 4760), (16, 264, 7096), (9, 4088, 3560)],
     (TILES, 64, 1): [(129, 216, 72), (17, 208, 72), (188, 216, 72)],
     (TILES, 64, 2): [(137, 904, 1416), (17, 912, 2936), (199, 912, 1416)],
     (TILES, 64, 3): [(129, 696, 712), (18, 664, 1416), (189, 656, 720)],
@@ -63,4 +67,4 @@ def form_of(lib, M, K, N, sms=SMS):
 
 
 def name(form):
-    return f"{'pairs' if form[0] == PAIRS else 'tiles'}-{form[1]}-{form[2]}"
+    return f"{('tokens', 'tiles', 'pairs')[form[0]]}-{form[1]}-{form[2]}"
