@@ -106,3 +106,8 @@ int launch_append(wave_kv* kv, int32_t n, const wave_entry* const* entries,
                   const void* const* K, const void* const* V, void* stream);
 
 }  // namespace wavei
+
+// CTAs per list (cut[0], a cluster) and clusters per list (cut[1]) of wave_token_attn on
+// a GPU of `sms` SMs, for `lists` lists of at most `longest` items. Host only; C
+// linkage, so that a test can ask.
+extern "C" void wavei_token_cut(int32_t sms, int64_t lists, int32_t longest, int32_t* cut);

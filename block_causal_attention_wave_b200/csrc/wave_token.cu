@@ -781,34 +781,6 @@ int launch_token_rows(const wave_kv* kv, const TokParams<CAP>& p, cudaStream_t s
   return p.h.rows_max <= 8 ? launch_token_any<1>(kv, p, s) : launch_token_any<2>(kv, p, s);
 }
 
-// CTAs per list (a cluster) and clusters per list for lists of at most `longest`
-// items.
-void cut_lists(TokHead& h, int32_t longest) {
-  // Clusters of 1 .. 8 such CTAs that a B200 holds at a time (occupancy query).
-  constexpr int kHeld[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
-  const int64_t lists = (int64_t)h.n_groups * h.heads;
-  h.parts = 1;
-  h.cluster = 1;
-  double best = 1e30;
-  for (int s = 1; s <= 8 && s <= std::max(1, longest); ++s) {
-    // Waves of clusters; in units of an item's time at a 148th of HBM's rate, an
-    // item takes 0.6 when an SM draws all it can, more once the SMs share HBM, and
-    // a wave two to start and end.
-    const double waves = (double)((lists + kHeld[s] - 1) / kHeld[s]);
-    const double active = (double)std::min<int64_t>(lists, kHeld[s]) * s;
-    const double t = waves * ((longest + s - 1) / s * std::max(0.6, active / 148.0) + 2.0);
-    if (t < best) best = t, h.cluster = s;
-  }
-  // Fewer than 8 long lists: several clusters each, while every CTA keeps eight
-  // items. The second kernel takes 6 us: one head over 41 chunks of 4680 tokens
-  // takes 28 us in 15 clusters, where one would draw 0.7 TB/s for 130; 8 lists of
-  // 290 items gain nothing (20 us and 20).
-  if (lists * 8 < 64 && longest >= 128) {
-    h.cluster = 8;
-    h.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(kHeld[8] / lists, longest / 64));
-  }
-}
-
 // Lists of a call: groups of consecutive queries with their distinct items.
 // kv->page_mark holds, per page, generation << 16 | index of the newest item of
 // that page in the group being built (items of one page with other counts are
@@ -882,7 +854,10 @@ int build_lists(wave_kv* kv, const wave_node* active, int32_t n, int32_t policy,
   }
   h.heads = H;
   h.per_kv = per_kv;
-  cut_lists(h, longest);
+  int32_t cut[2];
+  wavei_token_cut(kv->num_sms, (int64_t)h.n_groups * H, longest, cut);
+  h.cluster = cut[0];
+  h.parts = cut[1];
   return items;
 }
 
@@ -911,6 +886,31 @@ thread_local TokLists t_lists;  // large: keep off the stack; launches copy it
 }  // namespace wavei
 
 using namespace wavei;
+
+extern "C" void wavei_token_cut(int32_t sms, int64_t lists, int32_t longest, int32_t* cut) {
+  int32_t cluster = 1;
+  double best = 1e30;
+  for (int s = 1; s <= 8 && s <= std::max(1, longest); ++s) {
+    // Waves of clusters; in units of an item's time at one SM's share of HBM's rate, an
+    // item takes 0.6 when an SM draws all it can, more once the SMs share HBM, and
+    // a wave two to start and end.
+    const int64_t held = clusters_held(s, sms);
+    const double waves = (double)((lists + held - 1) / held);
+    const double active = (double)(std::min(lists, held) * s);
+    const double t = waves * ((longest + s - 1) / s * std::max(0.6, active / sms) + 2.0);
+    if (t < best) best = t, cluster = s;
+  }
+  cut[0] = cluster;
+  cut[1] = 1;
+  // Fewer than 8 long lists: several clusters each, while every CTA keeps eight
+  // items. The second kernel takes 6 us: one head over 41 chunks of 4680 tokens
+  // takes 28 us in 15 clusters, where one would draw 0.7 TB/s for 130; 8 lists of
+  // 290 items gain nothing (20 us and 20).
+  if (lists * 8 < 64 && longest >= 128) {
+    cut[0] = 8;
+    cut[1] = (int32_t)std::max<int64_t>(1, std::min<int64_t>(clusters_held(8, sms) / lists, longest / 64));
+  }
+}
 
 extern "C" int wave_token_attn_workspace(wave_kv* kv, const wave_node* active, int32_t n_active,
                                          int32_t policy, const int32_t* own_tokens,
