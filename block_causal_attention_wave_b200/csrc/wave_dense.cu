@@ -79,6 +79,20 @@ int allow_shared(const void* fn, int bytes, int device, std::atomic<uint64_t>& d
 
 using namespace wavei;
 
+extern "C" int wavei_kernel_registers(const void* fn, std::atomic<int32_t>* known, int32_t* regs) {
+  *regs = known->load(std::memory_order_relaxed);
+  if (*regs > 0) return WAVE_OK;
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, fn);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(WAVE_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
+  }
+  *regs = a.numRegs;
+  known->store(a.numRegs, std::memory_order_relaxed);
+  return WAVE_OK;
+}
+
 extern "C" void wavei_dense_form(int32_t sms, int32_t M, int32_t K, int32_t N, DenseForm* form) {
   *form = takes_tokens(sms, M, K, N) ? tokens_form(sms, M, K, N) : rows_form(sms, M, K, N);
 }

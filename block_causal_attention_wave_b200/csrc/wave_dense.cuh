@@ -221,6 +221,10 @@ int pair_rows_launch(const struct ::wave_kv* kv, const DenseArgs& a, int nt, int
 
 }  // namespace wavei
 
+// Registers a thread of kernel `fn`, asked for once and kept in the kernel's own word
+// `known` (0 until then; a failed query is returned, and asked again by the next call).
+extern "C" int wavei_kernel_registers(const void* fn, std::atomic<int32_t>* known, int32_t* regs);
+
 // The choice on a GPU of `sms` SMs. Host only; C linkage, so that a test can ask
 // which form its sizes reach.
 extern "C" void wavei_dense_form(int32_t sms, int32_t M, int32_t K, int32_t N, wavei::DenseForm* form);

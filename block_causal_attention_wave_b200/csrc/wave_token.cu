@@ -754,10 +754,9 @@ int launch_token(const TokParams<CAP>& p, int device, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const void* fn = reinterpret_cast<const void*>(&token_attn_kernel<D, FP8, QT, CAP>);
   if (int rc = allow_shared(fn, C::kSmemBytes, device, done)) return rc;
-  static const int regs = [fn] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, fn) == cudaSuccess ? fa.numRegs : 0;
-  }();
+  static std::atomic<int32_t> known{0};
+  int32_t regs;
+  if (int rc = wavei_kernel_registers(fn, &known, &regs)) return rc;
   // setmaxnreg.inc waits until registers are free: with fewer at launch than the
   // split assumes it would never return.
   if (D == 128 && regs < C::kRegsLaunch)
