@@ -17,7 +17,8 @@ import sysconfig
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libwave.so")
-CALL = os.path.join(PKG, "_call.so")
+# The name carries Python's ABI tag, so that another version does not load it.
+CALL = os.path.join(PKG, "_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -66,7 +67,12 @@ def build(verbose_ptxas: bool = False, out: str = LIB, defines=(), replace=None)
         raise RuntimeError("link of libwave.so failed")
     os.replace(tmp, out)
     if out == LIB:
-        build_call()
+        # The C library is whole without the binding's module: no reason to refuse it.
+        if os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+            build_call()
+        else:
+            sys.stderr.write("Python.h not found: the module _call, which KVCache's single-token "
+                             "calls need, is not built\n")
     return out
 
 
@@ -81,6 +87,9 @@ def build_call() -> str:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("g++ failed on wave_call.cpp")
     os.replace(CALL + ".tmp", CALL)
+    untagged = os.path.join(PKG, "_call.so")  # an earlier build's, which any version would load
+    if os.path.exists(untagged):
+        os.remove(untagged)
     return CALL
 
 
