@@ -243,7 +243,8 @@ int wave_linear(wave_kv* kv, const void* A, int32_t M, int32_t K, const void* W,
  * included, down to where their factor of x leaves float32's normal range (2^-126)
  * and the result is zero. wave_linear is the form without bias for whole rounds; this one
  * serves blocks whose projections carry a bias, widths that fill no tile, and
- * the single tokens that stream beside a round ([WS] "streaming unit").
+ * single tokens beside a round. (Single tokens are this library's own reading, here and
+ * in the calls below: the pages' smallest block is a streaming unit of many tokens.)
  * A: device bf16, M rows of K, row stride lda; W: device bf16 [N][K],
  * contiguous (a linear layer's [out][in] weight); bias: device bf16 [N] or
  * NULL; R: device bf16, M rows of N, row stride ldr, or NULL (added after
@@ -334,7 +335,10 @@ int wave_kv_free_pages(const wave_kv* kv, int32_t* n);
  * token with a non-zero value (1 if a = 0), else max(s, a / 448); kept tokens
  * become E4M3(code * s / s') and new ones E4M3(x / s'), each operation a
  * float32 one rounded to nearest, E4M3 as for WAVE_KV_FP8_E4M3. So values
- * already cached may be rounded once more whenever a larger token arrives.
+ * already cached may be rounded once more whenever a larger token arrives. A NaN is
+ * kept and does not enter a; an infinity makes the scale infinite, as in an append:
+ * every value of the page and head reads back as NaN until the infinite one is
+ * rewritten, and what was cached beside it is lost.
  * One launch for all entries. `entries`, `first`, `ntokens` are host arrays;
  * an entry is named once per call. ntokens[i] = 0 writes nothing. Strides in
  * elements, multiples of 8, >= H * d; 16-byte aligned pointers. Limits:
@@ -411,9 +415,9 @@ int wave_round_attn_split_workspace(wave_kv* kv, const wave_node* active, int32_
 
 /* Attention of single tokens over the cache: one query token for each listed
  * node, over the node's key list as wave_gather_table gives it, the own entry
- * up to own_tokens[i] tokens -- the step of a token that streams into a unit
- * while it is being written ([WS] "streaming unit", "K/V cache"), where
- * wave_round_attn takes a chunk's queries whole. For query i, query head x and
+ * up to own_tokens[i] tokens -- the step of a token that arrives while its entry is
+ * being written (over the cache of [WS] "K/V cache"; tokens one by one are this
+ * library's own reading), where wave_round_attn takes a chunk's queries whole. For query i, query head x and
  * its K/V head h = x / (q_heads / H):
  *   O_i[x] = softmax_k(Q_i[x] . K[k, h] / sqrt(d)) V[k, h]
  * own_tokens: host int32 [n_active], 0 <= own_tokens[i] <= the entry's tokens,
@@ -492,8 +496,8 @@ int wave_round_attn_static_scratch(wave_kv* kv, const wave_node* active, int32_t
 int wave_kv_last_launch_clock(wave_kv* kv, void* stream, int64_t* cycles, int64_t* ns);
 
 /* Bound on how long one wait inside a kernel launched on this handle may take
- * (attention and fused projection; the append kernel does not wait), in
- * nanoseconds; 0 restores the default of 2 s. A wait that runs out makes the
+ * (attention, projections, dense layers and token attention; appends, token writes and
+ * rotations do not wait), in nanoseconds; 0 restores the default of 2 s. A wait that runs out makes the
  * kernel stop every role, finish the copies and MMAs it has issued, free its
  * tensor memory and return; the launch's output is then undefined and the
  * next wave_kv_status reports WAVE_ERR_TIMEOUT. This is the failure-detection

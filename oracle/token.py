@@ -2,11 +2,12 @@
 
 TEST INFRASTRUCTURE ONLY (see the package docstring).
 
-A token that streams into a unit (Wan-Streamer v0.2 page, "streaming unit") runs
-the same block as a round's chunks: a dense layer, the rotary embedding at the
-token's own position, its K and V into the cache, attention over its node's key
-list as far as the list is written. The pages give no formulas; each is the
-plain one.
+A token that arrives while its unit is being written runs the same block as a
+round's chunks: a dense layer, the rotary embedding at the token's own position,
+its K and V into the cache, attention over its node's key list as far as the list
+is written. Tokens one by one are a reading of this library's own (the Wan-Streamer v0.2
+page's smallest block is a streaming unit of many tokens), and the pages give
+no formulas; each is the plain one.
 """
 from __future__ import annotations
 

@@ -241,3 +241,39 @@ def test_first_calls_inside_a_capture(cuda_lib, fmt):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", _FIRST, fmt], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
+
+
+def test_write_fp8_of_nan_and_infinity(cuda_lib):
+    """A NaN is kept and leaves the scale to the others; an infinity takes its page and
+    head with it until it is rewritten, and no other page or head."""
+    import torch
+    H, d, T = 2, 64, 200
+    kv = _cache(cuda_lib, H, d, T, 1, pages=2, fp8=True, fill=0xFF)
+    kv.alloc(0, 1)
+    x = torch.randn(T, H, d, device="cuda").bfloat16()
+
+    def read():
+        codes, scales = _pages(kv, (0, 1))
+        with np.errstate(invalid="ignore"):
+            v = quant.e4m3_decode(codes) * scales[..., None, None].astype(np.float64)
+        return v.transpose(0, 1, 3, 2, 4).reshape(2, -1, H, d)[:, :T], scales   # [K, V][token][head][d]
+    kv.write_tokens([(0, 1)], [0], x, x, [T])
+    before, scales = read()
+    y = x[:1].clone()
+    y[0, 0, 5] = float("nan")
+    kv.write_tokens([(0, 1)], [0], y, x[:1])
+    got, again = read()
+    assert np.isnan(got[0, 0, 0, 5]) and np.isnan(got).sum() == 1
+    got[0, 0, 0, 5] = before[0, 0, 0, 5]
+    assert np.array_equal(scales, again) and np.array_equal(got, before)
+    y[0, 0, 5] = float("inf")
+    kv.write_tokens([(0, 1)], [0], y, x[:1])
+    got, _ = read()
+    gone = np.zeros(got.shape, dtype=bool)
+    gone[0, :128, 0] = True
+    assert np.isnan(got[gone]).all() and np.array_equal(got[~gone], before[~gone])
+    kv.write_tokens([(0, 1)], [0], x[:1], x[:1])
+    got, _ = read()
+    gone[0, 0] = False
+    assert (got[gone] == 0).all() and np.array_equal(got[0, 128:], before[0, 128:])
+    assert (np.abs(got[0, 0] - torch_to_f64(x[0])) <= 2.0 ** -4 * np.abs(torch_to_f64(x[0])) + 2.0 ** -16).all()   # half steps; s < 2^-6
