@@ -1,8 +1,8 @@
 // The dense layer with bias where the wide GEMM's tiles would leave SMs idle:
 // single tokens, and rows up to a streaming unit.
 //
-// What both kernels compute: Y = act(A W^T + bias) (+ R), as the wide GEMM's
-// form with bias (wave_gemm.cu).
+// What both kernels compute: Y = act(A W^T + bias) (+ R), sums, bias, activation and
+// residual in fp32, one rounding to bf16.
 //
 // token_rows_kernel, up to 16 rows. Every weight is used once or a few times,
 // so the time is that of reading W from HBM, and for small layers that of one
@@ -77,14 +77,6 @@ __device__ __forceinline__ uint4 ld_rows(const uint16_t* p, bool in) {
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // WARPS: warps that share K; FT: n-tiles of 8 features per block; R16: more than 8 rows.
 template <int WARPS, int FT, bool R16, int ACT>
 __global__ void __launch_bounds__(32 * WARPS) token_rows_kernel(const __grid_constant__ TokenRowsParams p) {
@@ -138,8 +130,8 @@ __global__ void __launch_bounds__(32 * WARPS) token_rows_kernel(const __grid_con
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < FT; ++t) {
-        mma_bf16(acc[t], x0[at][u].x, x1[at][u].x, x0[at][u].y, x1[at][u].y, w[at][u][t].x, w[at][u][t].y);
-        mma_bf16(acc[t], x0[at][u].z, x1[at][u].z, x0[at][u].w, x1[at][u].w, w[at][u][t].z, w[at][u][t].w);
+        mma_16816<false>(acc[t], {x0[at][u].x, x1[at][u].x, x0[at][u].y, x1[at][u].y}, w[at][u][t].x, w[at][u][t].y);
+        mma_16816<false>(acc[t], {x0[at][u].z, x1[at][u].z, x0[at][u].w, x1[at][u].w}, w[at][u][t].z, w[at][u][t].w);
       }
   };
   constexpr int kStep = WARPS * U;
@@ -241,9 +233,6 @@ __device__ __forceinline__ void mma_slice(uint32_t d, uint32_t a, uint32_t b, ui
       : "memory");
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 template <int NF, int ACT>
 __global__ void __launch_bounds__(kSplitThreads, 1) split_rows_kernel(const __grid_constant__ SplitParams p) {
   using C = SplitCfg<NF>;

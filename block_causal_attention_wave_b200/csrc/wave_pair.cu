@@ -1,7 +1,6 @@
 // The dense layer with bias for many rows, on pairs of SMs.
 //
-// What it computes: Y = act(A W^T + bias) (+ R), as the other forms
-// (wave_few.cu, and wave_gemm.cu for the round's own layers).
+// What it computes: Y = act(A W^T + bias) (+ R), as the other forms (wave_few.cu).
 //
 // What bounds it: the tensor pipe, if the operands arrive. An SM takes in about
 // 60 bytes a clock through TMA; a 128 x 256 tile of one SM wants 48 KB per 512
@@ -70,9 +69,6 @@ struct PairParams {
   int32_t wide;
 };
 
-__device__ __forceinline__ void pair_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // `addr` of this CTA's shared memory, in the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t in_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -161,7 +157,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
   }
   tc_fence_before();
   __syncthreads();
-  pair_cluster_sync();  // every CTA's barriers exist before another CTA signals them
+  cluster_sync();  // every CTA's barriers exist before another CTA signals them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   chain_begin();
@@ -272,7 +268,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
     const int rows = max(0, min(128, p.M - mt * 256 - half * 128));
     const int cols = min(NT, p.N - nt * NT);
     const int per = max(1, (rows + p.splits - 1) / p.splits);
-    pair_cluster_sync();  // every CTA of the cluster is done with its ring
+    cluster_sync();  // every CTA of the cluster is done with its ring
     if (warp >= 2) {
       const int quarter = warp & 3, side = (warp - 2) >> 2;
       const int row = quarter * 32 + lane;
@@ -297,12 +293,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_rows_kernel(const __grid
     __syncwarp();
     sum_tiles<ACT, kPairThreads>(p, reinterpret_cast<const float*>(smem), p.splits, per, C::kPartRow,
                                  min(per, rows - pair * per), cols, (int64_t)mt * 256 + half * 128 + pair * per,
-                                 nt * NT, [] { __syncwarp(); pair_cluster_sync(); });
+                                 nt * NT, [] { __syncwarp(); cluster_sync(); });
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  pair_cluster_sync();  // neither CTA leaves while the other's MMAs or signals reach into it
+  cluster_sync();  // neither CTA leaves while the other's MMAs or signals reach into it
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");

@@ -49,9 +49,10 @@
 //   - bf16: P goes in as two bf16, its leading eight bits and the rest (what is
 //     dropped is below 2^-15 of it), one MMA each: rounded to one, the few
 //     weights of a peaked softmax would be off by up to 2^-8 each (seven chunks of 4680
-//     tokens, 12 heads: 34.4 us so, 34.7 with both). The rest of a weight is a positive number wherever the weight is
-//     (down to 2^-109), so that an infinite V that is seen gives an infinity, not the
-//     NaN of its product with zero.
+//     tokens, 12 heads: 34.4 us so, 34.7 with both; with more than eight query rows,
+//     whose products are twice as many, 5 to 10 % more). The rest of a weight is a
+//     positive number wherever the weight is (down to 2^-109), so that an infinite V
+//     that is seen gives an infinity, not the NaN of its product with zero.
 //   - Rows that do not see an item keep their O by selection, not by a zero
 //     weight, and V rows past the seen tokens are zeroed: whatever stands
 //     there, infinities and NaN included, reaches nothing.
@@ -151,20 +152,6 @@ struct TokCfg {
   static constexpr int kSteps = D / 16;   // k-steps of K Q^T
 };
 
-template <bool F16>
-__device__ __forceinline__ void tok_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -186,9 +173,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-__device__ __forceinline__ void tok_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // A float (pair) at shared address `addr` of the cluster's CTA `rank`.
 __device__ __forceinline__ float lds_rank(uint32_t addr, int rank) {
@@ -411,8 +395,8 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
                 const int st = (b * 2 + hh) * 2;
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
-                  tok_mma<false>(sc[t][kb], a0, qf[t][st][0], qf[t][st][1]);
-                  tok_mma<false>(sc[t][kb], a1, qf[t][st + 1][0], qf[t][st + 1][1]);
+                  mma_16816<false>(sc[t][kb], a0, qf[t][st][0], qf[t][st][1]);
+                  mma_16816<false>(sc[t][kb], a1, qf[t][st + 1][0], qf[t][st + 1][1]);
                 }
               }
         } else {
@@ -434,7 +418,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
                 const uint32_t a[4] = {e4m3_f16x2(wd[0][j] & 0xFFFF), e4m3_f16x2(wd[1][j] & 0xFFFF),
                                        e4m3_f16x2(wd[0][j] >> 16), e4m3_f16x2(wd[1][j] >> 16)};
 #pragma unroll
-                for (int t = 0; t < QT; ++t) tok_mma<true>(sc[t][kb], a, qf[t][hh * 4 + j][0], qf[t][hh * 4 + j][1]);
+                for (int t = 0; t < QT; ++t) mma_16816<true>(sc[t][kb], a, qf[t][hh * 4 + j][0], qf[t][hh * 4 + j][1]);
               }
             }
         }
@@ -518,23 +502,47 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
                 if (!WHOLE && key >= seen) v = make_uint4(0, 0, 0, 0);
                 x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
               }
+              uint32_t a[4][4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t a[4] = {__byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[0][e], x[1][e], 0x7632),
-                                       __byte_perm(x[2][e], x[3][e], 0x5410), __byte_perm(x[2][e], x[3][e], 0x7632)};
+                a[e][0] = __byte_perm(x[0][e], x[1][e], 0x5410);
+                a[e][1] = __byte_perm(x[0][e], x[1][e], 0x7632);
+                a[e][2] = __byte_perm(x[2][e], x[3][e], 0x5410);
+                a[e][3] = __byte_perm(x[2][e], x[3][e], 0x7632);
+              }
+              if constexpr (WHOLE) {
 #pragma unroll
-                for (int t = 0; t < QT; ++t) {
-                  float (&acc)[4] = o[t][b * 4 + e];
-                  if (WHOLE) {
-                    tok_mma<false>(acc, a, pr[t][kb][0], pr[t][kb][1]);
-                    tok_mma<false>(acc, a, pb[t][kb][0], pb[t][kb][1]);
-                  } else {
-                    float d[4] = {acc[0], acc[1], acc[2], acc[3]};
-                    tok_mma<false>(d, a, pr[t][kb][0], pr[t][kb][1]);
-                    tok_mma<false>(d, a, pb[t][kb][0], pb[t][kb][1]);
+                for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[c] = sees(t, c & 1) ? d[c] : acc[c];
+                  for (int t = 0; t < QT; ++t) {
+                    mma_16816<false>(o[t][b * 4 + e], a[e], pr[t][kb][0], pr[t][kb][1]);
+                    mma_16816<false>(o[t][b * 4 + e], a[e], pb[t][kb][0], pb[t][kb][1]);
                   }
+              } else {
+                // Two tiles of query rows: products apart, then added (16 queries over 632
+                // MB of pages: 120 us, else 125); one: carried through and selected (one
+                // token, 77 keys of its own: 5.32 us, else 5.45).
+#pragma unroll
+                for (int e0 = 0; e0 < 4; e0 += 2) {
+                  float d[2][QT][4] = {};
+                  if constexpr (QT == 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) d[i >> 2][0][i & 3] = o[0][b * 4 + e0 + (i >> 2)][i & 3];
+                  }
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) mma_16816<false>(d[e][t], a[e0 + e], pr[t][kb][0], pr[t][kb][1]);
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) {
+                      mma_16816<false>(d[e][t], a[e0 + e], pb[t][kb][0], pb[t][kb][1]);
+                      float (&acc)[4] = o[t][b * 4 + e0 + e];
+#pragma unroll
+                      for (int c = 0; c < 4; ++c)
+                        if (sees(t, c & 1)) acc[c] = QT == 1 ? d[e][t][c] : acc[c] + d[e][t][c];
+                    }
                 }
               }
             }
@@ -573,7 +581,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
                 const uint32_t a[4] = {e4m3_f16x2(k01 & 0xFFFF), e4m3_f16x2(k01 >> 16), e4m3_f16x2(k89 & 0xFFFF),
                                        e4m3_f16x2(k89 >> 16)};
 #pragma unroll
-                for (int t = 0; t < QT; ++t) tok_mma<true>(d[t], a, pb[t][kb][0], pb[t][kb][1]);
+                for (int t = 0; t < QT; ++t) mma_16816<true>(d[t], a, pb[t][kb][0], pb[t][kb][1]);
               }
 #pragma unroll
               for (int t = 0; t < QT; ++t)
@@ -675,7 +683,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
   // ---- join the cluster's CTAs, in rank order; rank r finishes every cluster-th
   // run of columns
   __syncwarp();
-  if (h.cluster > 1) tok_cluster_sync();
+  if (h.cluster > 1) cluster_sync();
   else consumers_sync<32 * C::kWarps>();
   constexpr int kWorkers = 32 * C::kWarps;
   for (int x = rank * kWorkers + threadIdx.x; x < grp.rows * D; x += h.cluster * kWorkers) {
@@ -705,7 +713,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, QT>::kThreads, 1)
     }
   }
   __syncwarp();
-  if (h.cluster > 1) tok_cluster_sync();  // no CTA leaves while another reads it
+  if (h.cluster > 1) cluster_sync();  // no CTA leaves while another reads it
 }
 
 // The join of a list's parts: one warp per (query, query head).
@@ -887,6 +895,8 @@ thread_local TokLists t_lists;  // large: keep off the stack; launches copy it
 using namespace wavei;
 
 extern "C" void wavei_token_cut(int32_t sms, int64_t lists, int32_t longest, int32_t* cut) {
+  // Of 20 cases measured (kept under profiles/) the choice is the best of clusters of
+  // 1 to 8 and of several clusters a list, or within 9 % of it.
   int32_t cluster = 1;
   double best = 1e30;
   for (int s = 1; s <= 8 && s <= std::max(1, longest); ++s) {
@@ -903,8 +913,7 @@ extern "C" void wavei_token_cut(int32_t sms, int64_t lists, int32_t longest, int
   cut[1] = 1;
   // Fewer than 8 long lists: several clusters each, while every CTA keeps eight
   // items. The second kernel takes 6 us: one head over 41 chunks of 4680 tokens
-  // takes 28 us in 15 clusters, where one would draw 0.7 TB/s for 130; 8 lists of
-  // 290 items gain nothing (20 us and 20).
+  // takes 25 us in 15 clusters, 108 in one; 8 lists of 71 items lose (10.8 us and 17.6).
   if (lists * 8 < 64 && longest >= 128) {
     cut[0] = 8;
     cut[1] = (int32_t)std::max<int64_t>(1, std::min<int64_t>(clusters_held(8, sms) / lists, longest / 64));

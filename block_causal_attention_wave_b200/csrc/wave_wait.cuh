@@ -30,12 +30,20 @@ __device__ __forceinline__ bool wait_within(uint32_t bar, uint32_t parity, const
 // so, and nothing of global memory is read or written before `chain_wait`, which
 // returns when the kernel before has ended and its writes are visible (to plain
 // loads and TMA: .nc loads ask for data that nothing writes while the kernel runs,
-// and the kernel before may). A kernel with tensor memory calls chain_begin when it
-// has its columns: the next one's allocation then waits for this one's end, never
-// this one's for the next. What is saved is a launch's latency and a prologue per
+// and the kernel before may). One exception: token_rows_kernel sends for weights into L2
+// ahead of the wait, where every SM's reads and writes meet, so that what the kernel
+// before still writes is written there. A kernel with tensor memory calls chain_begin
+// when it has its columns: the next one's allocation then waits for this one's end,
+// never this one's for the next. What is saved is a launch's latency and a prologue per
 // kernel of a token's step.
 __device__ __forceinline__ void chain_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// All threads of a cluster, whose writes to each other's shared memory are then seen. By
+// whole warps.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // A launch whose kernel begins with chain_begin and chain_wait; cluster: CTAs per
 // cluster (1: none).
