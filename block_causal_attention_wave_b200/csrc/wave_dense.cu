@@ -12,15 +12,16 @@ namespace {
 
 // Up to 16 rows: token_rows_kernel (wave_few.cu), by waves of its blocks: an SM holds
 // four of 8 warps (three with more than 8 rows), two of 16. Blocks of 8 features while
-// they are one wave, else of 16 (chained, weights from HBM, us, 8 and 16 features: 1536
-// -> 1536 3.2 and 4.3, 2048 -> 4736 4.7 and 6.0, 1536 -> 6144 6.6 and 5.6, 1536 -> 8960
-// 7.3 and 6.3, 8192 -> 8192 25.8 and 26.8). Sixteen warps to a block where that is one
-// wave and K is long (8 and 16 warps: 8960 -> 1536 11.2 and 8.4, 4096 -> 2048 5.7 and
-// 4.6, 2048 -> 1536 3.1 and 3.4, 4096 -> 4096 7.4 and 9.0).
-// With 9 to 16 rows a block reads more of A than of W, and tiles of 64 features take
-// over beyond one wave or where K is long (token rows and tiles: 16 rows 1536 -> 4608
-// 5.9 and 7.2, 4096 -> 4096 11.4 both, 8960 -> 1536 14.1 and 10.6, 8192 -> 8192 38.9
-// and 28.8; 12 rows 1536 -> 8960 9.8 and 8.4, 4096 -> 2048 6.9 and 8.5).
+// they are one wave, else of 16 (chained, weights from HBM, one row, us, 8 and 16
+// features: 1536 -> 1536 3.0 and 3.8, 2048 -> 4736 5.1 and 6.5, 1536 -> 8960 7.4 and
+// 6.2, 8192 -> 8192 25.8 and 25.7). Sixteen warps to a block where that is one wave and
+// K is long (8 and 16 warps: 8960 -> 1536 11.1 and 8.6, 4096 -> 2048 6.2 and 5.1, 1536
+// -> 1536 3.0 and 3.5, 4096 -> 4096 7.3 and 8.9).
+// With 9 to 16 rows a block reads more of A than of W, and tiles take over beyond one
+// wave or where K is long (token rows and the best tiles: 16 rows 1536 -> 4608 6.6 and
+// 7.6, 4096 -> 4096 11.8 both, 8960 -> 1536 14.3 and 11.0, 8192 -> 8192 39.3 and 26.7; 12
+// rows 1536 -> 8960 10.2 and 9.2, 4096 -> 2048 7.8 and 8.8). Of 40 sizes of up to 16 rows
+// measured, the rule takes the fastest form in each (the sweep is kept under profiles/).
 bool takes_tokens(int sms, int32_t M, int32_t K, int32_t N) { return M <= 8 || (M <= 16 && K <= 4096 && N <= 3 * 16 * sms); }
 DenseForm tokens_form(int sms, int32_t M, int32_t K, int32_t N) {
   const int held = M <= 8 ? 4 : 3;
@@ -30,13 +31,13 @@ DenseForm tokens_form(int sms, int32_t M, int32_t K, int32_t N) {
 
 // More rows: the cheapest form by its cost in us: a start and end, more where the
 // parts of K are joined, and what a 128-wide slice of K takes (for pairs in several
-// waves, at the clock under load). Against a sweep over M = 40 .. 4680 and K x N =
-// 1536 x 1536 .. 4096 x 4096 the choice is the best form or within a few percent
-// of it. Both sides: 984 x 8960 x 1536: 192-column pairs with K in two 29.9,
-// 256-column 34.5, 128-column tiles 38.6; 256 x 1536 x 1536: 64-column tiles with K
-// in two 8.4, 128-column in four 9.6, pairs 13; 512 x 1536 x 4608: 128-column tiles
-// 11.2, pairs 13.6; 2000 x 1536 x 8960: 256-column pairs 44, 192-column 50,
-// 128-column tiles 83.
+// waves, at the clock under load), fitted to 55 sizes, M = 40 .. 4680 and K x N = 1536 x
+// 1536 .. 4096 x 4096, of which it takes the best form in 49 and one within 7 % in the
+// others (the sweep is kept under profiles/). Both sides: 984 x 8960 x 1536: 192-column pairs with
+// K in two 29.8, 256-column 33.8, 128-column tiles 38.3; 256 x 1536 x 1536: 64-column
+// tiles with K in two 8.4, 128-column in four 9.6, pairs 11.8; 512 x 1536 x 4608:
+// 128-column tiles 11.2, pairs 13.6; 2000 x 1536 x 8960: 256-column pairs 43.5,
+// 192-column 49.3, 128-column tiles 82.
 DenseForm rows_form(int sms, int32_t M, int32_t K, int32_t N) {
   struct Form {
     int rows, cols, ctas, most;         // tile, CTAs that share one, most parts of K

@@ -14,8 +14,9 @@
 // What bounds it: HBM. A thread owns 16 bytes of a head (or 16 + 16 where the
 // partner sits d/2 away), works its sines and cosines out once and takes them
 // through several heads, whose loads are all in flight before the first store.
-// 18720 rows of 12 + 12 heads of 128 (230 MB): 37.2 us back to back, 6.2 TB/s, 0.94 of a
-// plain copy's rate; with load and store in turn a fifth more.
+// 18720 rows of 12 + 12 heads of 128 (230 MB): 37.6 us back to back, 6.1 TB/s, 0.93 of a
+// plain copy's rate (39.5 us with inputs of which L2 holds nothing); with load and store in
+// turn a fifth more.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -249,9 +250,9 @@ extern "C" int wave_rotary(wave_kv* kv, const wave_rotary_spec* spec, const int3
   p.rows = rows;
   turns_of(*spec, D, p);
   // A thread takes its angles through as many heads as leave the GPU about four
-  // blocks per SM, at most one batch (18720 rows of 12 + 12 heads of 128, us: 4
-  // heads a thread 47, 8 40.4, 24 41.2; 984 rows of 24 + 24 heads of 64: 1 9.5, 3
-  // 5.9, 8 6.7).
+  // blocks per SM, at most one batch (us, in a graph, inputs from HBM: 18720 rows of
+  // 12 + 12 heads of 128: 4 heads a thread 45.5, 8 39.5, 24 40.3; 984 rows of 24 + 24
+  // heads of 64, halves: 1 8.3, 3 4.8, 8 6.3).
   const int lanes = D / 2 / (spec->layout == WAVE_ROTARY_HALVES ? 8 : 4);
   const int64_t row_blocks = ((int64_t)rows * lanes + kRotaryThreads - 1) / kRotaryThreads;
   const int64_t groups = std::min<int64_t>(p.heads, (4LL * kv->num_sms + row_blocks - 1) / row_blocks);

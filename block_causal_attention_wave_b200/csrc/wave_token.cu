@@ -896,7 +896,7 @@ using namespace wavei;
 
 extern "C" void wavei_token_cut(int32_t sms, int64_t lists, int32_t longest, int32_t* cut) {
   // Of 20 cases measured (kept under profiles/) the choice is the best of clusters of
-  // 1 to 8 and of several clusters a list, or within 9 % of it.
+  // 1 to 8 and of several clusters a list, or within a tenth of it.
   int32_t cluster = 1;
   double best = 1e30;
   for (int s = 1; s <= 8 && s <= std::max(1, longest); ++s) {
