@@ -62,6 +62,16 @@ int check_query_node(const wave_kv* kv, wave_node node) {
   return WAVE_OK;
 }
 
+int check_history(const wave_kv* kv, wave_node node, int policy) {
+  // A list longer than the cache has a missing entry among its first size + 1.
+  const int span = history_span(node.chunk, kv->cfg.window);
+  if ((size_t)span <= kv->entries.size()) return WAVE_OK;
+  int r = span;
+  while (r > 1 && kv->entries.count(std::make_pair(node.chunk - r, phi(policy, node.level, r)))) --r;
+  return fail(WAVE_ERR_MISSING_KV, "K/V of (%d, %d) read by node (%d, %d) is not cached", node.chunk - r,
+              phi(policy, node.level, r), node.chunk, node.level);
+}
+
 int build_rows(const wave_kv* kv, const wave_node* active, int n, int policy,
                std::vector<int32_t>& rows, std::vector<int32_t>& offsets) {
   rows.clear();
@@ -69,6 +79,7 @@ int build_rows(const wave_kv* kv, const wave_node* active, int n, int policy,
   std::vector<std::pair<int32_t, int32_t>> ents;
   for (int i = 0; i < n; ++i) {
     int rc = check_query_node(kv, active[i]);
+    if (!rc) rc = check_history(kv, active[i], policy);
     if (rc) return rc;
     key_entries(kv, active[i], policy, ents);
     for (auto& e : ents) {

@@ -77,6 +77,10 @@ inline int64_t clusters_held(int ctas, int sms) {
   return std::max(1, kHeld[ctas] * sms / 148);
 }
 
+// WAVE_ERR_MISSING_KV if the node's history is longer than all the cache holds: found
+// without key_entries, whose list of it would be as long as its chunk's number.
+int check_history(const wave_kv* kv, wave_node node, int policy);
+
 // Device halves (defined in .cu files).
 int device_init(wave_kv* kv);
 // WAVE_ERR_ARG unless the calling thread's current device is the pool's: the

@@ -818,6 +818,7 @@ int build_lists(wave_kv* kv, const wave_node* active, int32_t n, int32_t policy,
     for (int32_t i = 0; i < nq; ++i) {
       const wave_node node = active[q0 + i];
       if (int rc = check_query_node(kv, node)) return rc;
+      if (int rc = check_history(kv, node, policy)) return rc;
       const uint16_t rows = (uint16_t)(((1u << per_kv) - 1) << (i * per_kv));
       key_entries(kv, node, policy, keys);
       for (size_t e = 0; e < keys.size(); ++e) {

@@ -277,3 +277,25 @@ def test_write_fp8_of_nan_and_infinity(cuda_lib):
     gone[0, 0] = False
     assert (got[gone] == 0).all() and np.array_equal(got[0, 128:], before[0, 128:])
     assert (np.abs(got[0, 0] - torch_to_f64(x[0])) <= 2.0 ** -4 * np.abs(torch_to_f64(x[0])) + 2.0 ** -16).all()   # half steps; s < 2^-6
+
+
+def test_token_attn_far_chunk(cuda_lib):
+    """A query of a chunk whose history the cache cannot hold is refused at once; a
+    window makes it an ordinary one."""
+    import resource
+    import torch
+    far = 2 ** 31 - 1
+    q = torch.ones(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    w = _World(cuda_lib, 1, 64, 100, 1, seed=41)
+    w.add(far, 1)
+    before = resource.getrusage(resource.RUSAGE_SELF).ru_maxrss
+    for call in (lambda: w.kv.token_attn([(far, 1)], "same", q, q.clone()),
+                 lambda: w.kv.token_attn_workspace([(far, 1)], "same")):
+        with pytest.raises(cuda_lib.WaveError) as e:
+            call()
+        assert e.value.code == -2
+    assert resource.getrusage(resource.RUSAGE_SELF).ru_maxrss - before < 1 << 18  # KB
+    w = _World(cuda_lib, 1, 64, 100, 1, window=1, seed=42)
+    w.add(far, 1)
+    w.add(far - 1, 1)
+    w.check([(far, 1)], "same", what="far chunk")
